@@ -131,7 +131,8 @@ def _quant(x, fmt, block):
     else:
         a = a.T.contiguous()
     a = a.clamp(min=TINY)
-    q = (x * _spread(TOP[fmt] / a, *x.shape, block)).to(F8[fmt])
+    f = torch.full_like(a, TOP[fmt]) / a     # not TOP / a, which torch computes as a reciprocal and a product
+    q = (x * _spread(f, *x.shape, block)).to(F8[fmt])
     return q, a / TOP[fmt]
 
 
