@@ -8,7 +8,9 @@ has no fallback: if the library is missing, every call raises.
 Functions with the C names take raw device pointers (ints) and a HIP stream
 handle and return the C status code. ``sgemm`` is the torch-tensor form: it
 derives sizes and leading dimensions from the tensors, enqueues on the current
-torch stream, and raises ``MisgemmError`` on a non-zero status.
+torch stream, and raises ``MisgemmError`` on a non-zero status. So are
+``fp8_gemm``, ``fp8_quantize``, ``rmsnorm`` and ``rmsnorm_backward`` for the
+8-bit linear layer (``include/misgemm_fp8.h``), from the module ``fp8``.
 """
 from __future__ import annotations
 
@@ -20,6 +22,8 @@ __all__ = [
     "mi_sgemm", "mi_sgemm_noalloc", "mi_sgemm_with_config", "mi_sgemm_select_config",
     "mi_sgemm_config_count", "mi_sgemm_config_name", "mi_sgemm_status_string",
     "mi_sgemm_release_workspace", "mi_clock_probe", "sgemm", "config_names",
+    "mi_fp8_gemm", "mi_fp8_quantize", "mi_rmsnorm", "mi_rmsnorm_backward",
+    "fp8_gemm", "fp8_quantize", "fp8_empty", "rmsnorm", "rmsnorm_backward",
 ]
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
@@ -68,6 +72,14 @@ def load_library():
     lib.mi_sgemm_release_workspace.restype = i
     lib.mi_clock_probe.argtypes = [i, p, ctypes.POINTER(i), p]
     lib.mi_clock_probe.restype = i
+    lib.mi_fp8_quantize.argtypes = [i, i, i, p, i, i, i, p, i, p, i, p, i, p, i, p]
+    lib.mi_fp8_quantize.restype = i
+    lib.mi_fp8_gemm.argtypes = [i, i, i, i, i, i, i, f, p, i, p, i, p, i, p, i, f, p, i, p]
+    lib.mi_fp8_gemm.restype = i
+    lib.mi_rmsnorm.argtypes = [i, i, i, i, p, i, p, i, p, f, p, i, p, i, i, p, i, p, i, p, p]
+    lib.mi_rmsnorm.restype = i
+    lib.mi_rmsnorm_backward.argtypes = [i, i, i, i, p, i, p, i, p, p, p, i, p, i, f, p, p]
+    lib.mi_rmsnorm_backward.restype = i
     _lib = lib
     return lib
 
@@ -224,3 +236,7 @@ def sgemm(transA: str, transB: str, alpha: float, A, B, beta: float, C, stream=N
     if rc != 0:
         raise MisgemmError(rc)
     return C
+
+
+from .fp8 import (fp8_empty, fp8_gemm, fp8_quantize, mi_fp8_gemm, mi_fp8_quantize,  # noqa: E402
+                  mi_rmsnorm, mi_rmsnorm_backward, rmsnorm, rmsnorm_backward)

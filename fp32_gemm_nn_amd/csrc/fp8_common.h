@@ -1,0 +1,110 @@
+// What the kernels of the 8-bit linear layer share: element types, eight
+// values at a time in and out of memory, block scales, reductions over lanes.
+#ifndef MISGEMM_FP8_COMMON_H
+#define MISGEMM_FP8_COMMON_H
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "misgemm_fp8.h"
+
+namespace misgemm_fp8 {
+
+using bf16 = __bf16;
+using f16 = _Float16;
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef bf16 bf16x2 __attribute__((ext_vector_type(2)));
+typedef bf16 bf16x4 __attribute__((ext_vector_type(4)));
+typedef bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef int i32x2 __attribute__((ext_vector_type(2)));
+typedef int i32x4 __attribute__((ext_vector_type(4)));
+typedef int i32x8 __attribute__((ext_vector_type(8)));
+
+constexpr int kBlock = 128;                  // values that share a scale
+constexpr float kTiny = 0x1p-100f;           // the least maximum a scale is made for
+
+__host__ __device__ constexpr int blocks(int n) { return n / kBlock + (n % kBlock != 0); }
+
+// The largest finite value of an 8-bit type.
+template <int FMT> __device__ constexpr float top() { return FMT == MI_E4M3 ? 448.0f : 57344.0f; }
+
+// Eight values of T as floats, or back, in 16-byte accesses (one for 16-bit
+// types, two for float) at any alignment of T: gfx950 reads and writes wide
+// words at any byte address. Values from `n` on are zero, and neither read
+// nor written.
+template <class T> struct Eight {
+    typedef T type __attribute__((ext_vector_type(8), aligned(sizeof(T))));
+};
+template <class T> __device__ __forceinline__ void load8(const T *p, int n, float (&v)[8]) {
+    if (n >= 8) {
+        const typename Eight<T>::type w = *reinterpret_cast<const typename Eight<T>::type *>(p);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = static_cast<float>(w[i]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = i < n ? static_cast<float>(p[i]) : 0.0f;
+    }
+}
+template <class T> __device__ __forceinline__ void store8(T *p, int n, const float (&v)[8]) {
+    if (n >= 8) {
+        typename Eight<T>::type w;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) w[i] = static_cast<T>(v[i]);
+        *reinterpret_cast<typename Eight<T>::type *>(p) = w;
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (i < n) p[i] = static_cast<T>(v[i]);
+    }
+}
+
+// Four floats to four 8-bit values, to nearest with ties to even. The values
+// are at most the type's largest by their scale (x * (T/a) exceeds T by two
+// roundings at most, which round back to T), so nothing saturates here.
+template <int FMT> __device__ __forceinline__ int pack4(float a, float b, float c, float d) {
+    int r = 0;
+    if constexpr (FMT == MI_E4M3) {
+        r = __builtin_amdgcn_cvt_pk_fp8_f32(a, b, r, false);
+        r = __builtin_amdgcn_cvt_pk_fp8_f32(c, d, r, true);
+    } else {
+        r = __builtin_amdgcn_cvt_pk_bf8_f32(a, b, r, false);
+        r = __builtin_amdgcn_cvt_pk_bf8_f32(c, d, r, true);
+    }
+    return r;
+}
+
+// N (8 or 16) bytes to memory at any address, the first `n` of them.
+template <int N> __device__ __forceinline__ void store_bytes(uint8_t *p, int n, const int (&w)[N / 4]) {
+    typedef int words __attribute__((ext_vector_type(N / 4), aligned(1)));
+    if (n >= N) {
+        words v;
+#pragma unroll
+        for (int i = 0; i < N / 4; ++i) v[i] = w[i];
+        *reinterpret_cast<words *>(p) = v;
+    } else {
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+            if (i < n) p[i] = static_cast<uint8_t>(static_cast<unsigned>(w[i / 4]) >> (8 * (i % 4)));
+    }
+}
+
+// Reductions over groups of 2^k neighbouring lanes, in every lane.
+template <int WIDTH> __device__ __forceinline__ float max_over(float v) {
+#pragma unroll
+    for (int o = 1; o < WIDTH; o *= 2) v = fmaxf(v, __shfl_xor(v, o));
+    return v;
+}
+template <int WIDTH> __device__ __forceinline__ float sum_over(float v) {
+#pragma unroll
+    for (int o = 1; o < WIDTH; o *= 2) v += __shfl_xor(v, o);
+    return v;
+}
+
+inline bool aligned(const void *p, size_t to) { return (reinterpret_cast<uintptr_t>(p) & (to - 1)) == 0; }
+inline bool is_real(int t) { return t == MI_F32 || t == MI_BF16 || t == MI_F16; }
+inline bool is_f8(int t) { return t == MI_E4M3 || t == MI_E5M2; }
+inline int launched() { return hipGetLastError() == hipSuccess ? MISGEMM_SUCCESS : MISGEMM_LAUNCH_FAILED; }
+
+}  // namespace misgemm_fp8
+
+#endif  // MISGEMM_FP8_COMMON_H

@@ -80,11 +80,13 @@
 #include <utility>
 
 #include "misgemm.h"
+#include "misgemm_fp8.h"
 #include "ladder.h"
 #include "scratch.h"
 #include "skinny_kernels.h"
 #include "tile_common.h"
 #include "tile_kernel.h"
+#include "workspace.h"
 
 namespace {
 
@@ -612,6 +614,8 @@ constexpr size_t kWsFloats = size_t(16) << 20;  // 64 MiB of partial blocks
 constexpr int kWsCounters = 1 << 16;
 static_assert(kWsFloats == misgemm_scratch::kPartialFloats && kWsCounters == misgemm_scratch::kCounters,
               "the static scratch has a stream workspace's capacity");
+static_assert(kWsFloats == misgemm_workspace::kFloats && kWsCounters == misgemm_workspace::kCounters,
+              "one workspace for every split product");
 
 struct Workspace {
     float *partials = nullptr;
@@ -1015,6 +1019,14 @@ int run(int config, char transA, char transB, int M, int N, int K, float alpha, 
 
 }  // namespace
 
+bool misgemm_workspace::get(hipStream_t stream, float **partials, int **counters) {
+    const Workspace *w = get_workspace(stream);
+    if (w == nullptr) return false;
+    *partials = w->partials;
+    *counters = w->counters;
+    return true;
+}
+
 extern "C" int mi_sgemm(char transA, char transB, int M, int N, int K, float alpha, const float *A, int lda,
                         const float *B, int ldb, float beta, float *C, int ldc, hipStream_t stream) {
     return run(-1, transA, transB, M, N, K, alpha, A, lda, B, ldb, beta, C, ldc, stream);
@@ -1087,6 +1099,15 @@ extern "C" const char *mi_sgemm_status_string(int status) {
         case MISGEMM_TOO_LARGE: return "problem too large (leading dimension beyond 32-bit tile offsets, or grid too large)";
         case MISGEMM_SCRATCH_TOO_SMALL: return "split plan needs more than the static scratch of mi_sgemm_noalloc holds";
         case MISGEMM_LAUNCH_FAILED: return "HIP kernel launch failed";
+        case MISGEMM_BAD_TYPE: return "an element type that this argument does not take";
+        case MISGEMM_BAD_BLOCK: return "unknown kind of scale block";
+        case MISGEMM_BAD_ROWS: return "rows < 0";
+        case MISGEMM_BAD_COLS: return "cols < 0";
+        case MISGEMM_NULL_INPUT: return "an input is null but would be read";
+        case MISGEMM_NULL_OUTPUT: return "an output that must be given is null";
+        case MISGEMM_NULL_SCALE: return "a scale table is null";
+        case MISGEMM_BAD_LD: return "a leading dimension smaller than its row";
+        case MISGEMM_BAD_LDS: return "a scale table's leading dimension smaller than its row";
         case MISGEMM_WORKSPACE_CAPTURED: return "workspace is used by a captured HIP graph and stays allocated until the process ends";
         default: return "unknown status";
     }
