@@ -28,35 +28,36 @@ __host__ __device__ constexpr int blocks(int n) { return n / kBlock + (n % kBloc
 // The largest finite value of an 8-bit type.
 template <int FMT> __device__ constexpr float top() { return FMT == MI_E4M3 ? 448.0f : 57344.0f; }
 
-// Eight values of T as floats, or back, in 16-byte accesses (one for 16-bit
-// types, two for float) at any alignment of T: gfx950 reads and writes wide
-// words at any byte address. Values from `n` on are zero, and neither read
-// nor written.
-template <class T> struct Eight {
-    typedef T type __attribute__((ext_vector_type(8), aligned(sizeof(T))));
+// N values of T as floats, or back, in accesses of up to 16 bytes at any
+// alignment of T: gfx950 reads and writes wide words at any byte address.
+// Values from `n` on are zero, and neither read nor written.
+template <class T, int N> struct Values {
+    typedef T type __attribute__((ext_vector_type(N), aligned(sizeof(T))));
 };
-template <class T> __device__ __forceinline__ void load8(const T *p, int n, float (&v)[8]) {
-    if (n >= 8) {
-        const typename Eight<T>::type w = *reinterpret_cast<const typename Eight<T>::type *>(p);
+template <class T, int N> __device__ __forceinline__ void load(const T *p, int n, float (&v)[N]) {
+    if (n >= N) {
+        const typename Values<T, N>::type w = *reinterpret_cast<const typename Values<T, N>::type *>(p);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = static_cast<float>(w[i]);
+        for (int i = 0; i < N; ++i) v[i] = static_cast<float>(w[i]);
     } else {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = i < n ? static_cast<float>(p[i]) : 0.0f;
+        for (int i = 0; i < N; ++i) v[i] = i < n ? static_cast<float>(p[i]) : 0.0f;
     }
 }
-template <class T> __device__ __forceinline__ void store8(T *p, int n, const float (&v)[8]) {
-    if (n >= 8) {
-        typename Eight<T>::type w;
+template <class T, int N> __device__ __forceinline__ void store(T *p, int n, const float (&v)[N]) {
+    if (n >= N) {
+        typename Values<T, N>::type w;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) w[i] = static_cast<T>(v[i]);
-        *reinterpret_cast<typename Eight<T>::type *>(p) = w;
+        for (int i = 0; i < N; ++i) w[i] = static_cast<T>(v[i]);
+        *reinterpret_cast<typename Values<T, N>::type *>(p) = w;
     } else {
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
+        for (int i = 0; i < N; ++i)
             if (i < n) p[i] = static_cast<T>(v[i]);
     }
 }
+template <class T> __device__ __forceinline__ void load8(const T *p, int n, float (&v)[8]) { load<T, 8>(p, n, v); }
+template <class T> __device__ __forceinline__ void store8(T *p, int n, const float (&v)[8]) { store<T, 8>(p, n, v); }
 
 // Four floats to four 8-bit values, to nearest with ties to even. The values
 // are at most the type's largest by their scale (x * (T/a) exceeds T by two

@@ -19,293 +19,14 @@
 // (1.9e-8 off) at half the rate.
 //
 // The product's first operand is B and its second A: a lane then holds
-// outputs of one row of A (one sA) at neighbouring columns, which it stores
-// as wide words. Which 32 values of k a lane group feeds does not matter as
+// outputs of one row of A (one sA) at neighbouring columns. Which 32 values of k a lane group feeds does not matter as
 // long as it is the same for both operands.
 
-#include "fp8_common.h"
-#include "workspace.h"
+#include "fp8_gemm.h"
 
 namespace {
 
 using namespace misgemm_fp8;
-
-constexpr int kNumCus = 256;
-constexpr int kXcds = 8;
-
-struct GemmArgs {
-    const uint8_t *A, *B;
-    const float *sa, *sb;
-    void *C;
-    float *ws;
-    int *counters;
-    long long lda, ldb, ldsa, ldsb, ldc;
-    int M, N, K;
-    int tiles_m, tiles_n, splits, kb_per_split;
-    float alpha, beta;
-    int ctype;
-    bool direct_a, direct_b;   // 16-byte aligned rows: copied to LDS without registers
-};
-
-// One operand's 128 bytes of k for ROWS rows in LDS: rows of eight 16-byte
-// chunks, chunk c of row r at position c ^ swz(r), so that the 16 rows a
-// fragment read touches spread over all banks. RUN: rows are read as four
-// runs of four neighbouring rows, RUN apart (0: sixteen neighbouring rows).
-template <int ROWS, int NT, int RUN> struct Stage {
-    static constexpr int PER = ROWS * 8 / NT;
-    static_assert(PER * NT == ROWS * 8, "whole chunks per thread");
-    static __device__ __forceinline__ int swz(int r) {
-        return RUN == 0 ? r & 7 : (r & 3) | ((r / (RUN == 0 ? 1 : RUN)) & 1) << 2;
-    }
-    // Rows past the matrix repeat its last one: their outputs are not stored.
-    static __device__ __forceinline__ void copy(const uint8_t *src, long long ld, int row0, int rows, int k0, int tid,
-                                                uint8_t *lds) {
-#pragma unroll
-        for (int j = 0; j < PER; ++j) {
-            const int idx = tid + NT * j, r = idx / 8, c = (idx % 8) ^ swz(r);
-            __builtin_amdgcn_global_load_lds(src + min(row0 + r, rows - 1) * ld + k0 + 16 * c,
-                                             lds + 16 * (NT * j + (tid & ~63)), 16, 0, 0);
-        }
-    }
-    // Any alignment, and the last block of k: bytes from K on are zero.
-    static __device__ __forceinline__ void copy_any(const uint8_t *src, long long ld, int row0, int rows, int k0, int K,
-                                                    int tid, uint8_t *lds) {
-        typedef int words __attribute__((ext_vector_type(4), aligned(1)));
-#pragma unroll
-        for (int j = 0; j < PER; ++j) {
-            const int idx = tid + NT * j, r = idx / 8, p = idx % 8, k = k0 + 16 * (p ^ swz(r));
-            const uint8_t *at = src + min(row0 + r, rows - 1) * ld + k;
-            i32x4 w = {0, 0, 0, 0};
-            if (k + 16 <= K) {
-                w = *reinterpret_cast<const words *>(at);
-            } else {
-                for (int b = 0; b < 16; ++b)
-                    if (k + b < K) w[b / 4] |= static_cast<int>(at[b]) << (8 * (b % 4));
-            }
-            *reinterpret_cast<i32x4 *>(lds + 16 * idx) = w;
-        }
-    }
-};
-
-// Lane values of one operand of a 16 x 16 x 128 product: the 32 bytes as they
-// are, or (EXACT) as BF16.
-template <bool EXACT> struct Operand {
-    i32x8 v;
-};
-template <> struct Operand<true> {
-    bf16x8 v[4];
-};
-
-template <int FMT> __device__ __forceinline__ bf16x8 widen(int lo, int hi) {
-    bf16x2 w[4];
-    if constexpr (FMT == MI_E4M3) {
-        w[0] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, 1.0f, false);
-        w[1] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, 1.0f, true);
-        w[2] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, 1.0f, false);
-        w[3] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, 1.0f, true);
-    } else {
-        w[0] = __builtin_amdgcn_cvt_scalef32_pk_bf16_bf8(lo, 1.0f, false);
-        w[1] = __builtin_amdgcn_cvt_scalef32_pk_bf16_bf8(lo, 1.0f, true);
-        w[2] = __builtin_amdgcn_cvt_scalef32_pk_bf16_bf8(hi, 1.0f, false);
-        w[3] = __builtin_amdgcn_cvt_scalef32_pk_bf16_bf8(hi, 1.0f, true);
-    }
-    const bf16x4 a = __builtin_shufflevector(w[0], w[1], 0, 1, 2, 3), b = __builtin_shufflevector(w[2], w[3], 0, 1, 2, 3);
-    return __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
-}
-
-// The 16-byte chunks at `at` and four chunks further of a row in LDS.
-template <int FMT, bool EXACT> __device__ __forceinline__ Operand<EXACT> fragment(const uint8_t *lds, int at) {
-    const i32x4 lo = *reinterpret_cast<const i32x4 *>(lds + at);
-    const i32x4 hi = *reinterpret_cast<const i32x4 *>(lds + (at ^ 64));
-    Operand<EXACT> o;
-    if constexpr (EXACT) {
-        o.v[0] = widen<FMT>(lo[0], lo[1]);
-        o.v[1] = widen<FMT>(lo[2], lo[3]);
-        o.v[2] = widen<FMT>(hi[0], hi[1]);
-        o.v[3] = widen<FMT>(hi[2], hi[3]);
-    } else {
-        o.v = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
-    }
-    return o;
-}
-
-// The builtin's operand selectors: 0 is E4M3, 1 is E5M2.
-template <int FA, int FB, bool EXACT>
-__device__ __forceinline__ f32x4 product(const Operand<EXACT> &a, const Operand<EXACT> &b) {
-    f32x4 p = {0.0f, 0.0f, 0.0f, 0.0f};
-    if constexpr (EXACT) {
-#pragma unroll
-        for (int s = 0; s < 4; ++s) p = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a.v[s], b.v[s], p, 0, 0, 0);
-        return p;
-    } else {
-        return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a.v, b.v, p, FA == MI_E5M2, FB == MI_E5M2, 0, 0, 0, 0);
-    }
-}
-
-// Eight neighbouring outputs of row m from column n on.
-template <class T> __device__ __forceinline__ void put8(const GemmArgs &g, int m, int n, float (&v)[8]) {
-    T *c = static_cast<T *>(g.C) + m * g.ldc + n;
-    if (g.beta != 0.0f) {
-        float old[8];
-        load8(c, g.N - n, old);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) v[j] = fmaf(g.beta, old[j], v[j]);
-    }
-    store8(c, g.N - n, v);
-}
-template <bool EXACT> __device__ __forceinline__ void put_row(const GemmArgs &g, int m, int n, float (&v)[8]) {
-    if (m >= g.M || n >= g.N) return;
-    if constexpr (EXACT)
-        put8<float>(g, m, n, v);
-    else if (g.ctype == MI_BF16)
-        put8<bf16>(g, m, n, v);
-    else
-        put8<f16>(g, m, n, v);
-}
-
-// The tile of workgroup `id`. Workgroups go round the XCDs in turn; each XCD
-// gets a run of tiles, eight rows of tiles at a time, so that its L2 serves
-// panels of A and B to neighbours.
-__device__ __forceinline__ void tile_of(int id, int tiles_m, int tiles_n, int &tm, int &tn) {
-    const int total = tiles_m * tiles_n, per = total / kXcds;
-    if (id < per * kXcds) id = (id % kXcds) * per + id / kXcds;
-    constexpr int GROUP = 8;
-    const int band = id / (GROUP * tiles_n), first = band * GROUP, height = min(GROUP, tiles_m - first);
-    const int in = id - band * GROUP * tiles_n;
-    tm = first + in % height;
-    tn = in / height;
-}
-
-// Tiles of BM x BN outputs on WM x WN waves, two buffers of one block of k
-// each. ROWB: B has a scale for each row and block. EXACT: C is FP32.
-template <int BM, int BN, int WM, int WN, int EU, int FA, int FB, bool ROWB, bool EXACT>
-__global__ __launch_bounds__(64 * WM * WN, EU) void fp8_tile(GemmArgs g) {
-    constexpr int NT = 64 * WM * WN, TM = BM / WM, TN = BN / WN, MI = TM / 16, NI = TN / 16;
-    static_assert(TN <= kBlock && kBlock % TN == 0 && NI % 2 == 0, "a wave's columns share a block");
-    using StageA = Stage<BM, NT, 0>;
-    using StageB = Stage<BN, NT, 4 * NI>;
-    __shared__ __align__(16) uint8_t lds[2][(BM + BN) * kBlock];
-    __shared__ int is_last;
-    const int tid = threadIdx.x, lane = tid % 64, wave = tid / 64;
-    const int i = lane % 16, grp = lane / 16;
-    const int wm = wave / WN, wn = wave % WN;
-
-    int tm, tn;
-    const int tiles = g.tiles_m * g.tiles_n;
-    const int split = blockIdx.x / tiles, tile = blockIdx.x - split * tiles;
-    tile_of(tile, g.tiles_m, g.tiles_n, tm, tn);
-    const int m0 = tm * BM, n0 = tn * BN;
-    const int kb0 = split * g.kb_per_split, kb1 = min(blocks(g.K), kb0 + g.kb_per_split);
-
-    const int row_a = wm * TM + i, row_b = wn * TN + (i / 4) * 4 * NI + i % 4;
-    const int at_a = row_a * kBlock + 16 * (grp ^ StageA::swz(row_a));
-    const int at_b = BM * kBlock + row_b * kBlock + 16 * (grp ^ StageB::swz(row_b));
-    const int ncol = n0 + wn * TN + grp * 4 * NI;   // this lane's 4*NI columns
-
-    auto stage = [&](int kb, int buf) {
-        uint8_t *to = lds[buf];
-        const bool whole = (kb + 1) * kBlock <= g.K;
-        if (whole && g.direct_a)
-            StageA::copy(g.A, g.lda, m0, g.M, kb * kBlock, tid, to);
-        else
-            StageA::copy_any(g.A, g.lda, m0, g.M, kb * kBlock, g.K, tid, to);
-        if (whole && g.direct_b)
-            StageB::copy(g.B, g.ldb, n0, g.N, kb * kBlock, tid, to + BM * kBlock);
-        else
-            StageB::copy_any(g.B, g.ldb, n0, g.N, kb * kBlock, g.K, tid, to + BM * kBlock);
-        asm volatile("" ::: "memory");
-    };
-
-    f32x4 acc[MI][NI];
-#pragma unroll
-    for (int a = 0; a < MI; ++a)
-#pragma unroll
-        for (int b = 0; b < NI; ++b) acc[a][b] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-
-    const float *sa = g.sa + m0 + wm * TM + i;
-    const int last_m = g.M - 1 - (m0 + wm * TM + i);
-    const float *sb = g.sb + min((n0 + wn * TN) / kBlock, blocks(g.N) - 1) * g.ldsb;
-
-    if (kb0 < kb1) stage(kb0, 0);
-    for (int kb = kb0; kb < kb1; ++kb) {
-        const int buf = (kb - kb0) & 1;
-        float fa[MI], fb[ROWB ? 4 * NI : 1];
-#pragma unroll
-        for (int a = 0; a < MI; ++a) fa[a] = sa[kb * g.ldsa + min(16 * a, last_m)];
-        if constexpr (ROWB) {
-#pragma unroll
-            for (int b = 0; b < 4 * NI; ++b) fb[b] = g.sb[kb * g.ldsb + min(ncol + b, g.N - 1)];
-        } else {
-            fb[0] = sb[kb];
-        }
-        __builtin_amdgcn_s_waitcnt(0);
-        __syncthreads();
-        if (kb + 1 < kb1) stage(kb + 1, buf ^ 1);
-        const uint8_t *from = lds[buf];
-        Operand<EXACT> fragb[NI];
-#pragma unroll
-        for (int b = 0; b < NI; ++b) fragb[b] = fragment<FB, EXACT>(from, at_b + b * 4 * kBlock);
-#pragma unroll
-        for (int a = 0; a < MI; ++a) {
-            // Without it the scheduler widens several rows ahead, beyond the registers.
-            if constexpr (EXACT) __builtin_amdgcn_sched_barrier(0);
-            const Operand<EXACT> fraga = fragment<FA, EXACT>(from, at_a + a * 16 * kBlock);
-#pragma unroll
-            for (int b = 0; b < NI; ++b) {
-                const f32x4 p = product<FB, FA, EXACT>(fragb[b], fraga);
-#pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    acc[a][b][j] = fmaf(p[j], ROWB ? fa[a] * fb[ROWB ? 4 * b + j : 0] : fa[a] * fb[0], acc[a][b][j]);
-            }
-        }
-    }
-
-    if (g.splits > 1) {
-        // Partial tiles go to the workspace, written and read past the XCDs'
-        // own caches; the last workgroup of a tile adds them in split order.
-        constexpr int PART = BM * BN;
-        float *part = g.ws + ((size_t)tile * g.splits) * PART + (size_t)wave * (MI * NI * 4 * 64) + lane;
-#pragma unroll
-        for (int a = 0; a < MI; ++a)
-#pragma unroll
-            for (int b = 0; b < NI; ++b)
-#pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    __hip_atomic_store(part + (size_t)split * PART + ((a * NI + b) * 4 + j) * 64, acc[a][b][j],
-                                       __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-        __builtin_amdgcn_s_waitcnt(0);
-        __syncthreads();
-        if (tid == 0)
-            is_last = __hip_atomic_fetch_add(&g.counters[tile], 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) ==
-                      g.splits - 1;
-        __syncthreads();
-        if (!is_last) return;
-        if (tid == 0) __hip_atomic_store(&g.counters[tile], 0, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-#pragma unroll
-        for (int a = 0; a < MI; ++a)
-#pragma unroll
-            for (int b = 0; b < NI; ++b) acc[a][b] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-        for (int s = 0; s < g.splits; ++s)
-#pragma unroll
-            for (int a = 0; a < MI; ++a)
-#pragma unroll
-                for (int b = 0; b < NI; ++b)
-#pragma unroll
-                    for (int j = 0; j < 4; ++j)
-                        acc[a][b][j] += __hip_atomic_load(part + (size_t)s * PART + ((a * NI + b) * 4 + j) * 64,
-                                                          __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-    }
-
-#pragma unroll
-    for (int a = 0; a < MI; ++a)
-#pragma unroll
-        for (int b = 0; b < NI; b += 2) {
-            float v[8];
-#pragma unroll
-            for (int j = 0; j < 8; ++j) v[j] = g.alpha * acc[a][b + j / 4][j % 4];
-            put_row<EXACT>(g, m0 + wm * TM + 16 * a + i, ncol + 4 * b, v);
-        }
-}
 
 // C <- beta * C where nothing is added.
 __global__ __launch_bounds__(256) void fp8_scale_c(GemmArgs g) {
@@ -314,41 +35,86 @@ __global__ __launch_bounds__(256) void fp8_scale_c(GemmArgs g) {
     for (int m = blockIdx.y; m < g.M; m += gridDim.y) {
         float v[8] = {};
         if (g.ctype == MI_F32)
-            put_row<true>(g, m, n, v);
+            put_row<true, 8>(g, m, n, v);
         else
-            put_row<false>(g, m, n, v);
+            put_row<false, 8>(g, m, n, v);
     }
 }
 
-template <int BM, int BN, int WM, int WN, int EU, int FA, int FB, bool ROWB, bool EXACT>
-int launch_tile(GemmArgs &g, int slots, hipStream_t stream) {
-    g.tiles_m = (g.M + BM - 1) / BM;
-    g.tiles_n = (g.N + BN - 1) / BN;
-    const int kblocks = blocks(g.K);
-    const long long tiles = (long long)g.tiles_m * g.tiles_n;
-    // Workgroups share a tile's k where the tiles leave half the slots empty,
-    // with at least four blocks of k each.
-    long long splits = slots / tiles;
-    if (splits > kblocks / 4) splits = kblocks / 4;
-    if (splits > 1 && tiles <= misgemm_workspace::kCounters) {
-        while (splits > 1 && (size_t)(tiles * splits) * BM * BN > misgemm_workspace::kFloats) --splits;
-        if (splits > 1 && !misgemm_workspace::get(stream, &g.ws, &g.counters)) splits = 1;
+// K < 16, which the tiles' 16-byte reads would pass: one output per thread,
+// the sum of its few products in order of k.
+template <int FMT> __device__ __forceinline__ float value(uint8_t v) {
+    if constexpr (FMT == MI_E4M3)
+        return __builtin_amdgcn_cvt_f32_fp8(v, 0);
+    else
+        return __builtin_amdgcn_cvt_f32_bf8(v, 0);
+}
+template <int FA, int FB> __global__ __launch_bounds__(256) void fp8_short(GemmArgs g, bool rows) {
+    const int n = blockIdx.x * 256 + threadIdx.x;
+    if (n >= g.N) return;
+    const float sb = g.sb[rows ? n : n / kBlock * g.ldsb];
+    for (int m = blockIdx.y; m < g.M; m += gridDim.y) {
+        float sum = 0.0f;
+        for (int k = 0; k < g.K; ++k)
+            sum = fmaf(value<FA>(g.A[m * g.lda + k]), value<FB>(g.B[n * g.ldb + k]), sum);
+        float v[1] = {g.alpha * (sum * (g.sa[m] * sb))};
+        if (g.ctype == MI_F32)
+            put_row<true, 1>(g, m, n, v);
+        else
+            put_row<false, 1>(g, m, n, v);
     }
-    if (splits < 1) splits = 1;
-    g.kb_per_split = (int)((kblocks + splits - 1) / splits);
-    g.splits = (kblocks + g.kb_per_split - 1) / g.kb_per_split;
-    hipLaunchKernelGGL((fp8_tile<BM, BN, WM, WN, EU, FA, FB, ROWB, EXACT>), dim3((unsigned)(tiles * g.splits)),
-                       dim3(64 * WM * WN), 0, stream, g);
-    return launched();
 }
 
-template <int FA, int FB, bool ROWB, bool EXACT> int launch(GemmArgs &g, hipStream_t stream) {
-    return launch_tile<128, 128, 2, 2, EXACT && ROWB ? 1 : 2, FA, FB, ROWB, EXACT>(g, 2 * kNumCus, stream);
-}
+// The kernel that is expected to be fastest: 0 to 5 are fp8_direct.hip's tile
+// shapes, 16 to 18 those of fp8_tile.hip.
+//
+// A product's time in us is taken to be first + round * (rounds - 1) + step *
+// rounds * steps, where a round is 256 workgroups (one for each CU) and a step
+// is a block of k for each of a workgroup's waves that split k. The constants
+// are fitted to the measured times of all kernels on 78 shapes (M, N and K
+// from 1, 64 and 64 to 8192, all types of C and kinds of scales), which they
+// reproduce to 8-17%; the kernel picked was within 1.2% of the fastest on
+// average, and 24% at worst.
+struct Cost {
+    int kernel, bm, bn, waves;
+    struct {
+        float first, round, step;
+    } fit[2];   // C of 16 bits; of 32, with BF16 products
+};
+constexpr Cost kCosts[] = {
+    {0, 16, 16, 16, {{2.4f, 0.40f, 0.88f}, {2.25f, 0.67f, 0.97f}}},
+    {1, 16, 32, 8, {{2.7f, 0.41f, 0.56f}, {2.5f, 0.96f, 0.79f}}},
+    {2, 32, 32, 8, {{2.8f, 0.48f, 0.78f}, {2.7f, 1.12f, 0.95f}}},
+    {3, 64, 32, 8, {{2.65f, 1.55f, 1.47f}, {2.8f, 2.06f, 1.60f}}},
+    {4, 64, 32, 4, {{3.4f, 0.41f, 0.69f}, {3.4f, 0.64f, 0.96f}}},
+    {5, 64, 64, 8, {{2.5f, 2.65f, 2.09f}, {}}},
+    {16, 128, 128, 1, {{4.7f, 2.24f, 0.72f}, {5.5f, 3.96f, 1.27f}}},
+    {17, 128, 128, 1, {{4.8f, 2.53f, 0.55f}, {5.8f, 3.47f, 0.95f}}},
+    {18, 256, 256, 1, {{6.7f, 12.5f, 1.42f}, {}}},
+};
+constexpr float kSplitCost = 7.0f;   // exchanging partial tiles
 
-template <int FA, int FB> int launch(bool rows, GemmArgs &g, hipStream_t stream) {
-    if (g.ctype == MI_F32) return rows ? launch<FA, FB, true, true>(g, stream) : launch<FA, FB, false, true>(g, stream);
-    return rows ? launch<FA, FB, true, false>(g, stream) : launch<FA, FB, false, false>(g, stream);
+int pick(const GemmArgs &g, bool rows) {
+    const bool exact = g.ctype == MI_F32, direct = g.lda < 1 << 26 && g.ldb < 1 << 26;
+    int best = 16;
+    float least = 3e38f;
+    for (const Cost &c : kCosts) {
+        const long long tiles = (g.M + c.bm - 1LL) / c.bm * ((g.N + c.bn - 1LL) / c.bn);
+        if (c.kernel < 16 && (!direct || tiles * 64 * c.waves >= 1LL << 32)) continue;
+        if (c.kernel == 5 && (exact || rows)) continue;   // does not fit the registers
+        if (c.kernel == 18 && exact) continue;
+        if (c.kernel >= 16 && (c.kernel > 16) != g.direct) continue;
+        const int splits = c.kernel == 16 || c.kernel == 17 ? splits_of(tiles, blocks(g.K)) : 1;
+        const float rounds = (float)((tiles * splits + kNumCus - 1) / kNumCus);
+        const float steps = (float)((blocks(g.K) + c.waves * splits - 1) / (c.waves * splits));
+        const auto &f = c.fit[exact];
+        const float us = f.first + f.round * (rounds - 1) + f.step * rounds * steps + (splits > 1 ? kSplitCost : 0.0f);
+        if (us < least) {
+            least = us;
+            best = c.kernel;
+        }
+    }
+    return best;
 }
 
 }  // namespace
@@ -399,8 +165,7 @@ extern "C" int mi_fp8_gemm(int atype, int btype, int block, int ctype, int M, in
     g.alpha = alpha;
     g.beta = beta;
     g.ctype = ctype;
-    g.direct_a = aligned(A, 16) && lda % 16 == 0;
-    g.direct_b = aligned(B, 16) && ldb % 16 == 0;
+    g.direct = aligned(A, 16) && lda % 16 == 0 && lda < 1 << 24 && aligned(B, 16) && ldb % 16 == 0 && ldb < 1 << 24;
     if (!reads) {
         if (beta == 1.0f) return MISGEMM_SUCCESS;
         hipLaunchKernelGGL(fp8_scale_c, dim3((unsigned)((N + 2047LL) / 2048), (unsigned)(M < 65535 ? M : 65535)),
@@ -408,7 +173,14 @@ extern "C" int mi_fp8_gemm(int atype, int btype, int block, int ctype, int M, in
         return launched();
     }
     const bool rows = block == MI_BLOCK_ROW;
-    if (atype == MI_E4M3)
-        return btype == MI_E4M3 ? launch<MI_E4M3, MI_E4M3>(rows, g, stream) : launch<MI_E4M3, MI_E5M2>(rows, g, stream);
-    return btype == MI_E4M3 ? launch<MI_E5M2, MI_E4M3>(rows, g, stream) : launch<MI_E5M2, MI_E5M2>(rows, g, stream);
+    if (K < 16) {
+        const dim3 grid((unsigned)((N + 255LL) / 256), (unsigned)(M < 65535 ? M : 65535));
+        const auto kernel = atype == MI_E4M3 ? (btype == MI_E4M3 ? fp8_short<MI_E4M3, MI_E4M3> : fp8_short<MI_E4M3, MI_E5M2>)
+                                             : (btype == MI_E4M3 ? fp8_short<MI_E5M2, MI_E4M3> : fp8_short<MI_E5M2, MI_E5M2>);
+        hipLaunchKernelGGL(kernel, grid, dim3(256), 0, stream, g, rows);
+        return launched();
+    }
+    const int kernel = pick(g, rows);
+    return kernel < 16 ? launch_direct(atype, btype, rows, kernel, g, stream)
+                       : launch_tiles(atype, btype, rows, kernel - 16, g, stream);
 }
