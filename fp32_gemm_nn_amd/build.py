@@ -1,6 +1,7 @@
 """Build the HIP library fp32_gemm_nn_amd/libmisgemm.so for gfx950.
 
-hipcc cross-compiles the device code without a GPU present. Packed-FP32 VALU
+The tensor forms' binding (_binding.so) is host code, compiled against torch's
+headers. hipcc cross-compiles the device code without a GPU present. Packed-FP32 VALU
 instructions are switched off for all device code. The sources are compiled
 to objects in parallel (under fp32_gemm_nn_amd/_build/) and linked into one
 shared library.
@@ -29,6 +30,26 @@ FLAGS = [
 ]
 
 
+BINDING_SRC = os.path.join(PKG, "csrc", "binding.cpp")
+BINDING = os.path.join(PKG, "_binding.so")
+CXX = os.environ.get("CXX", "g++")
+
+
+def binding_command(out: str) -> list[str]:
+    import sysconfig
+
+    import torch
+
+    home = os.path.dirname(torch.__file__)
+    libs = os.path.join(home, "lib")
+    return [CXX, "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden", "-Wall",
+            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+            "-isystem", os.path.join(home, "include"),
+            "-isystem", os.path.join(home, "include", "torch", "csrc", "api", "include"),
+            "-isystem", sysconfig.get_paths()["include"],
+            BINDING_SRC, "-o", out, "-L" + libs, "-ltorch_python", "-ltorch_cpu", "-lc10"]
+
+
 def build(verbose: bool = False, extra: list[str] | None = None) -> str:
     os.makedirs(OBJ_DIR, exist_ok=True)
     procs = []
@@ -40,6 +61,10 @@ def build(verbose: bool = False, extra: list[str] | None = None) -> str:
             print(" ".join(cmd), flush=True)
         procs.append((cmd, subprocess.Popen(cmd)))
         objs.append(obj)
+    cmd = binding_command(BINDING + ".tmp")
+    if verbose:
+        print(" ".join(cmd), flush=True)
+    procs.append((cmd, subprocess.Popen(cmd)))
     for cmd, p in procs:
         if p.wait() != 0:
             raise subprocess.CalledProcessError(p.returncode, cmd)
@@ -48,6 +73,7 @@ def build(verbose: bool = False, extra: list[str] | None = None) -> str:
         print(" ".join(link), flush=True)
     subprocess.run(link, check=True)
     os.replace(LIB + ".tmp", LIB)
+    os.replace(BINDING + ".tmp", BINDING)
     return LIB
 
 

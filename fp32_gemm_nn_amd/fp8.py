@@ -5,6 +5,8 @@ pointers (ints) and return the C status code. The tensor forms beside them
 check shapes, types, devices and overlap, enqueue on ``stream`` (default: the
 current torch stream of the tensors' device) and raise on an error. Outputs
 are tensors of the caller's, written in place; nothing is computed here.
+What is plainly right goes through a C++ binding in about a microsecond; the
+checks below name what is not, and decide the rest (memory that interleaves).
 
 An 8-bit matrix is a pair (q, scale): q of torch.float8_e4m3fn or
 torch.float8_e5m2 with contiguous rows, and a float32 table with a scale for
@@ -24,6 +26,32 @@ from . import MisgemmError, load_library
 _REAL = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
 _F8 = {torch.float8_e4m3fn: 3, torch.float8_e5m2: 4}
 _BLOCK = {"row": 0, "tile": 1}
+
+
+_native = None
+
+
+def _load_native():
+    """The tensor forms' C++ half (csrc/binding.cpp), bound to the library; raise if it is not built."""
+    global _native
+    import ctypes
+    import importlib.machinery
+    import importlib.util
+    import os
+
+    path = os.path.join(os.path.dirname(os.path.abspath(__file__)), "_binding.so")
+    lib = load_library()
+    if not os.path.exists(path):
+        raise RuntimeError(f"binding not built: {path} is missing. "
+                           "Run `python -m fp32_gemm_nn_amd.build` (or __graft_entry__.build()).")
+    loader = importlib.machinery.ExtensionFileLoader("_binding", path)
+    module = importlib.util.module_from_spec(importlib.util.spec_from_loader("_binding", loader))
+    loader.exec_module(module)
+    address = [ctypes.cast(f, ctypes.c_void_p).value
+               for f in (lib.mi_fp8_gemm, lib.mi_fp8_quantize, lib.mi_rmsnorm, lib.mi_rmsnorm_backward)]
+    module.bind(*address, getattr(torch._C, "_cuda_getCurrentRawStream", lambda index: None))
+    _native = module
+    return module
 
 
 def mi_fp8_quantize(xtype, rows, cols, x, ldx, ftype, block, q, ldq, scale, lds, qt, ldqt, scale_t, lds_t,
@@ -158,6 +186,10 @@ def fp8_quantize(x, q=None, scale=None, qt=None, scale_t=None, block: str = "row
     q = rn(x * (T / a)), with T = 448 (E4M3) or 57344 (E5M2). qt's row blocks run along x's rows.
     Returns the tensors that were given, in that order.
     """
+    rc = (_native or _load_native()).quantize(x, q, scale, qt, scale_t, block, stream)
+    if rc is not None:
+        _raise(rc, "mi_fp8_quantize")
+        return (q, scale) if qt is None else (qt, scale_t) if q is None else (q, scale, qt, scale_t)
     rows, cols = _matrix("x", x)
     dev = _on_device("x", x)
     a = _Arg("x", x, x.shape, _REAL, dev)
@@ -191,6 +223,10 @@ def fp8_gemm(alpha: float, A, scale_a, B, scale_b, beta: float, C, block: str = 
     scale_a has a scale for each row and 128 of k; scale_b is a table of kind ``block``. C is M x N in
     float32, bfloat16 or float16; blocks are scaled and added in FP32. beta == 0: C is not read.
     """
+    rc = (_native or _load_native()).gemm(alpha, A, scale_a, B, scale_b, beta, C, block, stream)
+    if rc is not None:
+        _raise(rc, "mi_fp8_gemm")
+        return C
     M, K = _matrix("A", A)
     N = _matrix("B", B)[0]
     dev = _on_device("A", A)
@@ -216,6 +252,9 @@ def rmsnorm(x, weight, eps: float, residual=None, h=None, y=None, q=None, scale=
     h, y, (q, scale) and rstd are written where given (y or q must be). h may be x or residual itself.
     q is quantised from y in FP32, with scales of kind "row". rstd is for ``rmsnorm_backward``.
     """
+    rc = (_native or _load_native()).rmsnorm(x, weight, eps, residual, h, y, q, scale, rstd, stream)
+    if rc is not None:
+        return _raise(rc, "mi_rmsnorm")
     rows, cols = _matrix("x", x)
     dev = _on_device("x", x)
     size, types = x.element_size(), (x.dtype,)
@@ -256,6 +295,9 @@ def rmsnorm_backward(dy, h, weight, rstd, dx, dweight=None, dh=None, beta: float
     dy, h, dx and dh share a type; h and rstd are as ``rmsnorm`` wrote them. dx may be dy or dh itself.
     dweight is float32, or None where it is not wanted.
     """
+    rc = (_native or _load_native()).rmsnorm_backward(dy, h, weight, rstd, dx, dweight, dh, beta, stream)
+    if rc is not None:
+        return _raise(rc, "mi_rmsnorm_backward")
     rows, cols = _matrix("dy", dy)
     dev = _on_device("dy", dy)
     size, types = dy.element_size(), (dy.dtype,)

@@ -142,3 +142,17 @@ def test_overlap():
         fp8._apart([arg(buf[5, 3:9])], [left])
     fp8._apart([arg(buf[5, 40:50])], [left])
     fp8._apart([arg(buf[:0])], [arg(buf)])
+
+
+def test_binding_leaves_host_tensors():
+    """What is not on a device is not taken by the binding; the tensor form names the argument."""
+    torch = pytest.importorskip("torch")
+    from fp32_gemm_nn_amd import fp8
+
+    native = fp8._load_native()
+    q, s = torch.zeros(4, 128).to(torch.float8_e4m3fn), torch.ones(1, 4)
+    assert native.gemm(1.0, q, s, q, s, 0.0, torch.zeros(4, 4), "row", None) is None
+    assert native.quantize(torch.zeros(4, 128), q, s, None, None, "row", None) is None
+    assert native.gemm() is None and native.rmsnorm(1) is None and native.rmsnorm_backward(*[None] * 9) is None
+    with pytest.raises(ValueError, match="A must be a device tensor"):
+        mg.fp8_gemm(1.0, q, s, q, s, 0.0, torch.zeros(4, 4), block="row")
