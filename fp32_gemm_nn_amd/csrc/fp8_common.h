@@ -89,16 +89,37 @@ template <int N> __device__ __forceinline__ void store_bytes(uint8_t *p, int n, 
     }
 }
 
-// Reductions over groups of 2^k neighbouring lanes, in every lane.
+// Reductions over groups of 16 or 64 neighbouring lanes, in every lane. In 16
+// the partners come by rotations in the same instruction.
+template <int BY> __device__ __forceinline__ float rotated16(float v) {
+    return __builtin_bit_cast(
+        float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), 0x120 + BY, 0xf, 0xf, false));
+}
 template <int WIDTH> __device__ __forceinline__ float max_over(float v) {
-#pragma unroll
-    for (int o = 1; o < WIDTH; o *= 2) v = fmaxf(v, __shfl_xor(v, o));
+    static_assert(WIDTH == 16 || WIDTH == 64, "");
+    v = fmaxf(v, rotated16<8>(v));
+    v = fmaxf(v, rotated16<4>(v));
+    v = fmaxf(v, rotated16<2>(v));
+    v = fmaxf(v, rotated16<1>(v));
+    if constexpr (WIDTH == 64) {
+        v = fmaxf(v, __shfl_xor(v, 16));
+        v = fmaxf(v, __shfl_xor(v, 32));
+    }
     return v;
 }
-template <int WIDTH> __device__ __forceinline__ float sum_over(float v) {
-#pragma unroll
-    for (int o = 1; o < WIDTH; o *= 2) v += __shfl_xor(v, o);
+__device__ __forceinline__ float sum_over64(float v) {
+    v += rotated16<8>(v);
+    v += rotated16<4>(v);
+    v += rotated16<2>(v);
+    v += rotated16<1>(v);
+    v += __shfl_xor(v, 16);
+    v += __shfl_xor(v, 32);
     return v;
+}
+// The value of lane I of each 16.
+template <int I> __device__ __forceinline__ float of16(float v) {
+    return __builtin_bit_cast(float,
+                              __builtin_amdgcn_mov_dpp(__builtin_bit_cast(int, v), 0x150 + I, 0xf, 0xf, true));
 }
 
 inline bool aligned(const void *p, size_t to) { return (reinterpret_cast<uintptr_t>(p) & (to - 1)) == 0; }
