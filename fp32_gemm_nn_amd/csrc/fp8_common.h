@@ -59,6 +59,58 @@ template <class T, int N> __device__ __forceinline__ void store(T *p, int n, con
 template <class T> __device__ __forceinline__ void load8(const T *p, int n, float (&v)[8]) { load<T, 8>(p, n, v); }
 template <class T> __device__ __forceinline__ void store8(T *p, int n, const float (&v)[8]) { store<T, 8>(p, n, v); }
 
+// Eight values of T as they lie in memory, of which the first `n` of a row of
+// `cols` values are wanted (others zero; n may be negative): one wide read
+// without a branch, so that reads ahead of their use stay so. Where fewer than
+// eight are left, the row's last eight are read and moved. `col` is where in
+// the row; cols >= 8. EVEN: cols is a multiple of 8, so that n is 8 or none.
+template <class T, bool EVEN> struct Eight {
+    typedef typename Values<T, 8>::type type;
+    typedef int words __attribute__((ext_vector_type(2 * sizeof(T))));
+    type v;
+    __device__ __forceinline__ void fetch(const T *row, int col, int cols) {
+        v = *reinterpret_cast<const type *>(row + min(col, cols - 8));
+    }
+    // Down by BY values, where `over` has that bit.
+    template <int BY> static __device__ __forceinline__ words moved(words w, int over) {
+        constexpr int N = 2 * sizeof(T), STEP = BY * (int)sizeof(T) / 4;
+        words m;
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            if constexpr (STEP > 0)
+                m[i] = i + STEP < N ? w[i + STEP < N ? i + STEP : 0] : 0;
+            else
+                m[i] = (int)((uint32_t)w[i] >> 16 | (i + 1 < N ? (uint32_t)w[i + 1 < N ? i + 1 : 0] << 16 : 0u));
+        }
+#pragma unroll
+        for (int i = 0; i < N; ++i) w[i] = (over & BY) ? m[i] : w[i];
+        return w;
+    }
+    // After `fetch`, at the first use.
+    __device__ __forceinline__ void settle(int col, int cols) {
+        const int over = max(col + 8 - cols, 0);
+        words w = __builtin_bit_cast(words, v);
+        if constexpr (EVEN) {
+#pragma unroll
+            for (unsigned i = 0; i < 2 * sizeof(T); ++i) w[i] = over > 0 ? 0 : w[i];
+        } else {
+            // No branch here either.
+            w = moved<4>(w, over);
+            w = moved<2>(w, over);
+            w = moved<1>(w, over);
+#pragma unroll
+            for (unsigned i = 0; i < 2 * sizeof(T); ++i) w[i] = over >= 8 ? 0 : w[i];
+        }
+        v = __builtin_bit_cast(type, w);
+    }
+    // Has the values made into floats anew from here on, not kept as such.
+    __device__ __forceinline__ void again() {
+        words w = __builtin_bit_cast(words, v);
+        asm("" : "+v"(w));
+        v = __builtin_bit_cast(type, w);
+    }
+};
+
 // Four floats to four 8-bit values, to nearest with ties to even. The values
 // are at most the type's largest by their scale (x * (T/a) exceeds T by two
 // roundings at most, which round back to T), so nothing saturates here.
@@ -89,7 +141,7 @@ template <int N> __device__ __forceinline__ void store_bytes(uint8_t *p, int n, 
     }
 }
 
-// Reductions over groups of 16 or 64 neighbouring lanes, in every lane. In 16
+// Reductions over groups of 16, 32 or 64 neighbouring lanes, in every lane. In 16
 // the partners come by rotations in the same instruction.
 template <int BY> __device__ __forceinline__ float rotated16(float v) {
     return __builtin_bit_cast(
@@ -107,13 +159,14 @@ template <int WIDTH> __device__ __forceinline__ float max_over(float v) {
     }
     return v;
 }
-__device__ __forceinline__ float sum_over64(float v) {
+template <int WIDTH> __device__ __forceinline__ float sum_over(float v) {
+    static_assert(WIDTH == 16 || WIDTH == 32 || WIDTH == 64, "");
     v += rotated16<8>(v);
     v += rotated16<4>(v);
     v += rotated16<2>(v);
     v += rotated16<1>(v);
-    v += __shfl_xor(v, 16);
-    v += __shfl_xor(v, 32);
+    if constexpr (WIDTH >= 32) v += __shfl_xor(v, 16);
+    if constexpr (WIDTH >= 64) v += __shfl_xor(v, 32);
     return v;
 }
 // The value of lane I of each 16.

@@ -55,22 +55,29 @@ __global__ __launch_bounds__(256) void quantize(QuantArgs a) {
     const int rb = blockIdx.y, cb = blockIdx.x;
     const int row0 = rb * kBlock + tr * 8, col0 = cb * kBlock + tc * 8;
     const int nc = min(8, max(0, a.cols - col0));
-    const T *x = static_cast<const T *>(a.x) + row0 * a.ldx + col0;
+    const T *x = static_cast<const T *>(a.x);
 
-    typename Values<T, 8>::type v[8];
-    if (nc == 8 && row0 + 8 <= a.rows) {
+    // The same for the whole workgroup, and without a branch for each value:
+    // reads past an edge are of the last row and the row's last eight values.
+    Eight<T, false> v[8];
+    if ((cb + 1) * kBlock <= a.cols && (rb + 1) * kBlock <= a.rows) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = *reinterpret_cast<const typename Values<T, 8>::type *>(x + i * a.ldx);
+        for (int i = 0; i < 8; ++i) v[i].fetch(x + (row0 + i) * a.ldx, col0, a.cols);
+    } else if (a.cols >= 8) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i].fetch(x + min(row0 + i, a.rows - 1) * a.ldx, col0, a.cols);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i].settle(row0 + i < a.rows ? col0 : a.cols, a.cols);
     } else {
 #pragma unroll
         for (int i = 0; i < 8; ++i)
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
-                v[i][j] = static_cast<T>(0.0f);
-                if (row0 + i < a.rows && j < nc) v[i][j] = x[i * a.ldx + j];
+                v[i].v[j] = static_cast<T>(0.0f);
+                if (row0 + i < a.rows && j < nc) v[i].v[j] = x[(row0 + i) * a.ldx + col0 + j];
             }
     }
-    auto value = [&](int i, int j) { return static_cast<float>(v[i][j]); };
+    auto value = [&](int i, int j) { return static_cast<float>(v[i].v[j]); };
 
     float rowf[8];   // T / maximum, of each row
     float tilef = 0.0f;

@@ -6,7 +6,8 @@
 // 4096 in BF16: the norm with residual, h, y and 8 bits takes 59 us (5.1 TB/s),
 // the gradients 50 us (5.4 TB/s) and 5 us for the sum of the partial ones; a
 // copy of 256 MiB reaches 5.4 TB/s here. One row of 4096 takes 3.6 us, of
-// which a launch is 2 to 3.
+// which a launch is 2 to 3; 333 x 1300 in FP32 with the weight's gradient in
+// the same launch 5.2 us.
 
 #include "fp8_common.h"
 #include "workspace.h"
@@ -28,42 +29,21 @@ struct NormArgs {
     float eps;
 };
 
-// Eight values of T as they lie in memory, fetched a row ahead of their use.
-// EVEN: the row's length is a multiple of 8, so that there are eight or none.
-template <class T, bool EVEN> struct Raw {
-    typename Values<T, 8>::type v;
-    // Has the values made into floats anew from here on, not kept as such.
-    __device__ __forceinline__ void again() {
-        typedef int words __attribute__((ext_vector_type(2 * sizeof(T))));
-        words w = __builtin_bit_cast(words, v);
-        asm("" : "+v"(w));
-        v = __builtin_bit_cast(typename Values<T, 8>::type, w);
-    }
-    __device__ __forceinline__ void fetch(const T *p, int n) {
-        if (EVEN ? n > 0 : n >= 8) {
-            v = *reinterpret_cast<const typename Values<T, 8>::type *>(p);
-        } else {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                v[i] = static_cast<T>(0.0f);
-                if constexpr (!EVEN)
-                    if (i < n) v[i] = p[i];
-            }
-        }
-    }
-};
-
-// Sum over the W waves of a row, in each of its threads, in a fixed order.
+// Sum over the NT threads of a row, in each of them, in a fixed order.
 // `part` is not reused before another barrier.
-template <int W> __device__ __forceinline__ float row_sum(float v, float *part) {
-    v = sum_over64(v);
-    if constexpr (W == 1) return v;
-    if (threadIdx.x % 64 == 0) part[threadIdx.x / 64 % W] = v;
-    __syncthreads();
-    v = part[0];
+template <int NT> __device__ __forceinline__ float row_sum(float v, float *part) {
+    v = sum_over<(NT < 64 ? NT : 64)>(v);
+    if constexpr (NT <= 64) {
+        return v;
+    } else {
+        constexpr int W = NT / 64;
+        if (threadIdx.x % 64 == 0) part[threadIdx.x / 64 % W] = v;
+        __syncthreads();
+        v = part[0];
 #pragma unroll
-    for (int w = 1; w < W; ++w) v += part[w];
-    return v;
+        for (int w = 1; w < W; ++w) v += part[w];
+        return v;
+    }
 }
 
 // y of eight values, y and q out. The 16 lanes that hold 128 columns share a scale.
@@ -99,31 +79,31 @@ __device__ __forceinline__ void norm_in(const NormArgs &a, long long row, int co
     }
 }
 
-// W waves take a row, PER eights of its columns per thread in registers, and a
+// NT threads take a row, PER eights of its columns each in registers, and a
 // workgroup G rows at a time, `turns` times. The weight stays in registers
 // (read for each row it would be a quarter of what a row moves), and the next
 // row's x and residual are on their way while this one is reduced and written.
-template <class T, class TW, int FMT, int W, int G, int PER, bool EVEN>
-__global__ __launch_bounds__(64 * W * G) void rmsnorm(NormArgs a) {
-    constexpr int NT = 64 * W;
+template <class T, class TW, int FMT, int NT, int G, int PER, bool EVEN>
+__global__ __launch_bounds__(NT *G) void rmsnorm(NormArgs a) {
     // Two turns of partial sums: a wave still reading one row's is at most one
     // barrier behind the wave that writes the next row's.
-    __shared__ float parts[2][G][W];
+    __shared__ float parts[2][G][NT > 64 ? NT / 64 : 1];
     const int tid = threadIdx.x % NT, group = threadIdx.x / NT;
-    Raw<TW, EVEN> w[PER];
-    Raw<T, EVEN> x[PER], r[PER];
+    Eight<TW, EVEN> w[PER];
+    Eight<T, EVEN> x[PER], r[PER];
 #pragma unroll
     for (int p = 0; p < PER; ++p) {
         const int col = (tid + NT * p) * 8;
-        w[p].fetch(static_cast<const TW *>(a.weight) + col, a.cols - col);
+        w[p].fetch(static_cast<const TW *>(a.weight), col, a.cols);
+        w[p].settle(col, a.cols);
     }
     auto fetch = [&](long long row) {
         row = row < a.rows ? row : a.rows - 1;   // past the end: not used
 #pragma unroll
         for (int p = 0; p < PER; ++p) {
             const int col = (tid + NT * p) * 8;
-            x[p].fetch(static_cast<const T *>(a.x) + row * a.ldx + col, a.cols - col);
-            if (a.res != nullptr) r[p].fetch(static_cast<const T *>(a.res) + row * a.ldr + col, a.cols - col);
+            x[p].fetch(static_cast<const T *>(a.x) + row * a.ldx, col, a.cols);
+            if (a.res != nullptr) r[p].fetch(static_cast<const T *>(a.res) + row * a.ldr, col, a.cols);
         }
     };
     long long row = blockIdx.x * (long long)G + group;
@@ -132,6 +112,8 @@ __global__ __launch_bounds__(64 * W * G) void rmsnorm(NormArgs a) {
         float h[PER][8], sum = 0.0f;
 #pragma unroll
         for (int p = 0; p < PER; ++p) {
+            x[p].settle((tid + NT * p) * 8, a.cols);
+            if (a.res != nullptr) r[p].settle((tid + NT * p) * 8, a.cols);
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
                 h[p][j] = static_cast<float>(x[p].v[j]);
@@ -142,7 +124,7 @@ __global__ __launch_bounds__(64 * W * G) void rmsnorm(NormArgs a) {
         }
         const long long next = row + (long long)gridDim.x * G;
         if (t + 1 < a.turns) fetch(next);
-        const float rstd = 1.0f / sqrtf(row_sum<W>(sum, parts[t & 1][group]) / a.cols + a.eps);
+        const float rstd = 1.0f / sqrtf(row_sum<NT>(sum, parts[t & 1][group]) / a.cols + a.eps);
         if (row < a.rows) {
             if (a.rstd != nullptr && tid == 0) a.rstd[row] = rstd;
 #pragma unroll
@@ -160,7 +142,7 @@ __global__ __launch_bounds__(64 * W * G) void rmsnorm(NormArgs a) {
     }
 }
 
-// Rows too long for registers: each is read twice.
+// Rows too long for registers (or shorter than eight values): each is read twice.
 template <class T, class TW, int FMT>
 __global__ __launch_bounds__(64 * kMaxWaves) void rmsnorm_long(NormArgs a) {
     constexpr int NT = 64 * kMaxWaves;
@@ -177,7 +159,7 @@ __global__ __launch_bounds__(64 * kMaxWaves) void rmsnorm_long(NormArgs a) {
 #pragma unroll
             for (int j = 0; j < 8; ++j) sum = fmaf(h[j], h[j], sum);
         }
-        const float rstd = 1.0f / sqrtf(row_sum<kMaxWaves>(sum, parts[turn]) / a.cols + a.eps);
+        const float rstd = 1.0f / sqrtf(row_sum<NT>(sum, parts[turn]) / a.cols + a.eps);
         if (a.rstd != nullptr && tid == 0) a.rstd[row] = rstd;
         // Each thread writes h where it alone reads x and the residual, after
         // it has read them: h may be either.
@@ -194,28 +176,32 @@ __global__ __launch_bounds__(64 * kMaxWaves) void rmsnorm_long(NormArgs a) {
     }
 }
 
-template <class T, class TW, int FMT, int W, int G, int PER> int launch_rows(NormArgs a, hipStream_t stream) {
+template <class T, class TW, int FMT, int NT, int G, int PER> int launch_rows(NormArgs a, hipStream_t stream) {
     // As many workgroups as the CUs hold at once (16 waves of them each, 24
     // where a thread has 8 columns), and as even a number of rows for each as
     // that allows.
-    constexpr long long kPlaces = kNumCus * ((PER == 2 ? 16 : 24) / (W * G));
+    constexpr long long kPlaces = kNumCus * ((PER == 2 ? 1024 : 1536) / (NT * G));
     const long long sets = ((long long)a.rows + G - 1) / G;
     a.turns = (int)((sets + kPlaces - 1) / kPlaces);
     const dim3 grid((unsigned)((sets + a.turns - 1) / a.turns));
     if (a.cols % 8 == 0)
-        hipLaunchKernelGGL((rmsnorm<T, TW, FMT, W, G, PER, true>), grid, dim3(64 * W * G), 0, stream, a);
+        hipLaunchKernelGGL((rmsnorm<T, TW, FMT, NT, G, PER, true>), grid, dim3(NT * G), 0, stream, a);
     else
-        hipLaunchKernelGGL((rmsnorm<T, TW, FMT, W, G, PER, false>), grid, dim3(64 * W * G), 0, stream, a);
+        hipLaunchKernelGGL((rmsnorm<T, TW, FMT, NT, G, PER, false>), grid, dim3(NT * G), 0, stream, a);
     return launched();
 }
 
 template <class T, class TW, int FMT> int launch_norm(const NormArgs &a, hipStream_t stream) {
-    if (a.cols <= 512) return launch_rows<T, TW, FMT, 1, 4, 1>(a, stream);
-    if (a.cols <= 1024) return launch_rows<T, TW, FMT, 2, 2, 1>(a, stream);
-    if (a.cols <= 2048) return launch_rows<T, TW, FMT, 4, 1, 1>(a, stream);
-    if (a.cols <= 4096) return launch_rows<T, TW, FMT, 4, 1, 2>(a, stream);
-    if (a.cols <= 8192) return launch_rows<T, TW, FMT, 8, 1, 2>(a, stream);
-    if (a.cols <= 16384) return launch_rows<T, TW, FMT, 16, 1, 2>(a, stream);
+    if (a.cols >= 8 && a.cols <= 16384) {
+        if (a.cols <= 128) return launch_rows<T, TW, FMT, 16, 16, 1>(a, stream);
+        if (a.cols <= 256) return launch_rows<T, TW, FMT, 32, 8, 1>(a, stream);
+        if (a.cols <= 512) return launch_rows<T, TW, FMT, 64, 4, 1>(a, stream);
+        if (a.cols <= 1024) return launch_rows<T, TW, FMT, 128, 2, 1>(a, stream);
+        if (a.cols <= 2048) return launch_rows<T, TW, FMT, 256, 1, 1>(a, stream);
+        if (a.cols <= 4096) return launch_rows<T, TW, FMT, 256, 1, 2>(a, stream);
+        if (a.cols <= 8192) return launch_rows<T, TW, FMT, 512, 1, 2>(a, stream);
+        return launch_rows<T, TW, FMT, 1024, 1, 2>(a, stream);
+    }
     // A grid of 2^20 workgroups stays within the 2^32 threads of a launch.
     const dim3 grid((unsigned)(a.rows < (1 << 20) ? a.rows : 1 << 20));
     hipLaunchKernelGGL((rmsnorm_long<T, TW, FMT>), grid, dim3(64 * kMaxWaves), 0, stream, a);
@@ -257,26 +243,92 @@ __device__ __forceinline__ void back_out(const BackArgs &a, long long row, int c
     store8(static_cast<T *>(a.dx) + row * a.lddx + col, n, dx);
 }
 
-// W waves take a row, PER eights of its columns per thread, and a workgroup G
+// The weight's gradient of 64 columns from dy and h themselves, by NT threads:
+// eight columns to a thread, NT / 8 rows at a time, whose sums are added in order.
+template <class T, int NT> __device__ __forceinline__ void grad_columns(const BackArgs &a, int block) {
+    constexpr int ROWS = NT / 8;
+    __shared__ float part[ROWS][64];
+    const int lane = threadIdx.x % 8, first = threadIdx.x / 8;
+    const int col = block * 64 + lane * 8;
+    float sum[8] = {};
+    if (a.cols >= 8) {
+        // Four rows at once, by every thread alike: past the end the last one's, for nothing.
+        for (long long r0 = 0; r0 < a.rows; r0 += 4 * ROWS) {
+            Eight<T, false> dy[4], h[4];
+            float rstd[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const long long at = r0 + i * ROWS + first, row = at < a.rows ? at : a.rows - 1;
+                dy[i].fetch(static_cast<const T *>(a.dy) + row * a.lddy, col, a.cols);
+                h[i].fetch(static_cast<const T *>(a.h) + row * a.ldh, col, a.cols);
+                rstd[i] = a.rstd[row];
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                dy[i].settle(col, a.cols);
+                h[i].settle(col, a.cols);
+                if (r0 + i * ROWS + first < a.rows) {
+#pragma unroll
+                    for (int j = 0; j < 8; ++j)
+                        sum[j] = fmaf(static_cast<float>(dy[i].v[j]), static_cast<float>(h[i].v[j]) * rstd[i], sum[j]);
+                }
+            }
+        }
+    } else {
+        for (long long row = first; row < a.rows; row += ROWS) {
+            float dy[8], h[8];
+            load8(static_cast<const T *>(a.dy) + row * a.lddy + col, a.cols - col, dy);
+            load8(static_cast<const T *>(a.h) + row * a.ldh + col, a.cols - col, h);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) sum[j] = fmaf(dy[j], h[j] * a.rstd[row], sum[j]);
+        }
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j) part[first][lane * 8 + j] = sum[j];
+    __syncthreads();
+    // Eight threads add a column's sums of neighbouring rows each, then one theirs.
+    const int c = threadIdx.x % 64, eighth = threadIdx.x / 64;
+    static_assert(ROWS % (NT / 64) == 0 && NT / 64 >= 1, "");
+    constexpr int EACH = ROWS / (NT / 64);
+    float s = 0.0f;
+#pragma unroll
+    for (int r = 0; r < EACH; ++r) s += part[eighth * EACH + r][c];
+    __syncthreads();
+    part[eighth][c] = s;
+    __syncthreads();
+    if (eighth == 0 && block * 64 + c < a.cols) {
+#pragma unroll
+        for (int r = 1; r < NT / 64; ++r) s += part[r][c];
+        float *dw = a.dweight + block * 64 + c;
+        *dw = a.beta == 0.0f ? s : fmaf(a.beta, *dw, s);
+    }
+}
+
+// NT threads take a row, PER eights of its columns each, and a workgroup G
 // rows at a time, `turns` times; the next row's operands are on their way
 // while this one is reduced and written. Each thread keeps its columns' share
 // of the weight's gradient, and the workgroup writes one row of `partials`.
 // AHEAD: there are registers for that.
-template <class T, class TW, int W, int G, int PER, bool EVEN, bool AHEAD>
-__global__ __launch_bounds__(64 * W * G) void rmsnorm_back(BackArgs a) {
-    constexpr int NT = 64 * W;
+template <class T, class TW, int NT, int G, int PER, bool EVEN, bool AHEAD>
+__global__ __launch_bounds__(NT *G) void rmsnorm_back(BackArgs a) {
+    // Workgroups past the rows', where there are some: the weight's gradient.
+    if ((int)blockIdx.x >= a.groups) {
+        grad_columns<T, NT * G>(a, blockIdx.x - a.groups);
+        return;
+    }
     // Two turns of sums: a wave still reading one row's is at most one
     // barrier behind the wave that writes the next row's.
-    __shared__ float parts[2][G][W];
+    __shared__ float parts[2][G][NT > 64 ? NT / 64 : 1];
     __shared__ float shares[G > 1 ? G - 1 : 1][G > 1 ? NT * PER * 8 : 1];
     const int tid = threadIdx.x % NT, group = threadIdx.x / NT;
-    Raw<TW, EVEN> wr[PER];
-    Raw<T, EVEN> dyr[PER], hr[PER], dhr[PER];
+    Eight<TW, EVEN> wr[PER];
+    Eight<T, EVEN> dyr[PER], hr[PER], dhr[PER];
     float dw[PER][8], rstd = 0.0f;
 #pragma unroll
     for (int p = 0; p < PER; ++p) {
         const int col = (tid + NT * p) * 8;
-        wr[p].fetch(static_cast<const TW *>(a.weight) + col, a.cols - col);
+        wr[p].fetch(static_cast<const TW *>(a.weight), col, a.cols);
+        wr[p].settle(col, a.cols);
 #pragma unroll
         for (int j = 0; j < 8; ++j) dw[p][j] = 0.0f;
     }
@@ -285,10 +337,10 @@ __global__ __launch_bounds__(64 * W * G) void rmsnorm_back(BackArgs a) {
         rstd = a.rstd[row];
 #pragma unroll
         for (int p = 0; p < PER; ++p) {
-            const int col = (tid + NT * p) * 8, n = a.cols - col;
-            dyr[p].fetch(static_cast<const T *>(a.dy) + row * a.lddy + col, n);
-            hr[p].fetch(static_cast<const T *>(a.h) + row * a.ldh + col, n);
-            if (AHEAD && a.dh != nullptr) dhr[p].fetch(static_cast<const T *>(a.dh) + row * a.lddh + col, n);
+            const int col = (tid + NT * p) * 8;
+            dyr[p].fetch(static_cast<const T *>(a.dy) + row * a.lddy, col, a.cols);
+            hr[p].fetch(static_cast<const T *>(a.h) + row * a.ldh, col, a.cols);
+            if (AHEAD && a.dh != nullptr) dhr[p].fetch(static_cast<const T *>(a.dh) + row * a.lddh, col, a.cols);
         }
     };
     long long row = blockIdx.x * (long long)G + group;
@@ -298,9 +350,12 @@ __global__ __launch_bounds__(64 * W * G) void rmsnorm_back(BackArgs a) {
         const bool live = row < a.rows;
         const float scale = rstd;
         float sum = 0.0f;
-        Raw<T, EVEN> dy[PER], h[PER], dh[PER];
+        Eight<T, EVEN> dy[PER], h[PER], dh[PER];
 #pragma unroll
         for (int p = 0; p < PER; ++p) {
+            dyr[p].settle((tid + NT * p) * 8, a.cols);
+            hr[p].settle((tid + NT * p) * 8, a.cols);
+            if (AHEAD && a.dh != nullptr) dhr[p].settle((tid + NT * p) * 8, a.cols);
             dy[p] = dyr[p];
             h[p] = hr[p];
             dh[p] = dhr[p];
@@ -311,18 +366,22 @@ __global__ __launch_bounds__(64 * W * G) void rmsnorm_back(BackArgs a) {
         }
         const long long next = row + (long long)a.groups * G;
         if (AHEAD && t + 1 < a.turns) fetch(next);
-        const float mean = row_sum<W>(sum, parts[t & 1][group]) / a.cols;
+        const float mean = row_sum<NT>(sum, parts[t & 1][group]) / a.cols;
         if (live) {
 #pragma unroll
             for (int p = 0; p < PER; ++p) {
                 const int col = (tid + NT * p) * 8;
                 float dx[8];
                 dy[p].again();
-                if (!AHEAD && sizeof(T) == 4)   // no registers for it: L2 has it still
-                    h[p].fetch(static_cast<const T *>(a.h) + row * a.ldh + col, a.cols - col);
+                if (!AHEAD && sizeof(T) == 4) {   // no registers for it: L2 has it still
+                    h[p].fetch(static_cast<const T *>(a.h) + row * a.ldh, col, a.cols);
+                    h[p].settle(col, a.cols);
+                }
                 h[p].again();
-                if (!AHEAD && a.dh != nullptr)
-                    dh[p].fetch(static_cast<const T *>(a.dh) + row * a.lddh + col, a.cols - col);
+                if (!AHEAD && a.dh != nullptr) {
+                    dh[p].fetch(static_cast<const T *>(a.dh) + row * a.lddh, col, a.cols);
+                    dh[p].settle(col, a.cols);
+                }
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
                     const float d = static_cast<float>(dy[p].v[j]), u = static_cast<float>(h[p].v[j]) * scale;
@@ -360,7 +419,8 @@ __global__ __launch_bounds__(64 * W * G) void rmsnorm_back(BackArgs a) {
     }
 }
 
-// Rows too long for registers: dx alone, each row read twice.
+// Rows too long for registers (or shorter than eight values): dx alone, each
+// row read twice.
 template <class T, class TW>
 __global__ __launch_bounds__(64 * kMaxWaves) void rmsnorm_back_long(BackArgs a) {
     constexpr int NT = 64 * kMaxWaves;
@@ -378,7 +438,7 @@ __global__ __launch_bounds__(64 * kMaxWaves) void rmsnorm_back_long(BackArgs a) 
 #pragma unroll
             for (int j = 0; j < 8; ++j) sum = fmaf(dy[j] * w[j], u[j] * rstd, sum);
         }
-        const float mean = row_sum<kMaxWaves>(sum, parts[turn]) / a.cols;
+        const float mean = row_sum<NT>(sum, parts[turn]) / a.cols;
         for (long long c = threadIdx.x * 8; c < a.cols; c += NT * 8) {
             const int col = (int)c, n = a.cols - col;
             float dy[8], u[8], w[8], dw[8] = {};
@@ -392,24 +452,9 @@ __global__ __launch_bounds__(64 * kMaxWaves) void rmsnorm_back_long(BackArgs a) 
     }
 }
 
-// The weight's gradient of 64 columns from dy and h themselves: four waves
-// sum every fourth row each. For what has no partial sums.
-template <class T>
-__global__ __launch_bounds__(256) void weight_grad(BackArgs a) {
-    __shared__ float part[4][64];
-    const int lane = threadIdx.x % 64, wave = threadIdx.x / 64;
-    const int col = blockIdx.x * 64 + lane;
-    float sum = 0.0f;
-    if (col < a.cols)
-        for (long long row = wave; row < a.rows; row += 4)
-            sum = fmaf(static_cast<float>(static_cast<const T *>(a.dy)[row * a.lddy + col]),
-                       static_cast<float>(static_cast<const T *>(a.h)[row * a.ldh + col]) * a.rstd[row], sum);
-    part[wave][lane] = sum;
-    __syncthreads();
-    if (wave == 0 && col < a.cols) {
-        sum = ((part[0][lane] + part[1][lane]) + part[2][lane]) + part[3][lane];
-        a.dweight[col] = a.beta == 0.0f ? sum : fmaf(a.beta, a.dweight[col], sum);
-    }
+// The weight's gradient alone.
+template <class T, int NT> __global__ __launch_bounds__(NT) void weight_grad(BackArgs a) {
+    grad_columns<T, NT>(a, blockIdx.x);
 }
 
 // Partial rows summed: 16 columns per workgroup, four to a thread, of which 64
@@ -449,14 +494,37 @@ __global__ __launch_bounds__(256) void sum_partials(BackArgs a) {
 
 constexpr int kGroups = 2 * kNumCus;   // workgroups of the backward pass, and partial rows
 
-template <class T, class TW, int W, int G, int PER> int launch_back_rows(BackArgs a, hipStream_t stream) {
+// Threads to a row of the backward pass, and rows of a workgroup.
+inline int back_threads(int cols) {
+    int nt = 16;
+    while (nt < 512 && nt * 8 < cols) nt *= 2;
+    return cols > 8192 ? 1024 : nt;
+}
+inline int back_rows(int cols) { return cols > 8192 ? 1 : 512 / back_threads(cols); }
+
+// Whether the weight's gradient is formed from dy and h by workgroups of its
+// own, in the same launch, rather than from partial sums in a second one. The
+// first costs 4.5 ns a row (its workgroups take all rows one after another),
+// the second 2.6 us and the partial sums' way to memory and back at 2.4 TB/s:
+// 600 x 4096 in BF16 take 9.1 and 13.9 us, 2000 x 512 take 13.0 and 6.9 us.
+inline bool few_rows(const BackArgs &a) {
+    const long long sets = ((long long)a.rows + back_rows(a.cols) - 1) / back_rows(a.cols);
+    const long long groups = sets < kGroups ? sets : kGroups;
+    return 4.5e-3 * a.rows < 2.6 + 8.0 * groups * a.cols / 2.4e6;
+}
+
+template <class T, class TW, int NT, int PER> int launch_back_rows(BackArgs a, hipStream_t stream) {
+    constexpr int G = NT == 1024 ? 1 : 512 / NT;
     const long long sets = ((long long)a.rows + G - 1) / G;
     a.turns = (int)((sets + kGroups - 1) / kGroups);
     a.groups = (int)((sets + a.turns - 1) / a.turns);
+    const bool own = a.dweight != nullptr && a.partials == nullptr;
+    const dim3 grid((unsigned)(a.groups + (own ? (a.cols + 63) / 64 : 0)));
+    constexpr bool AHEAD = NT * PER < 2048;
     if (a.cols % 8 == 0)
-        hipLaunchKernelGGL((rmsnorm_back<T, TW, W, G, PER, true, W * PER < 32>), dim3(a.groups), dim3(64 * W * G), 0, stream, a);
+        hipLaunchKernelGGL((rmsnorm_back<T, TW, NT, G, PER, true, AHEAD>), grid, dim3(NT * G), 0, stream, a);
     else
-        hipLaunchKernelGGL((rmsnorm_back<T, TW, W, G, PER, false, W * PER < 32>), dim3(a.groups), dim3(64 * W * G), 0, stream, a);
+        hipLaunchKernelGGL((rmsnorm_back<T, TW, NT, G, PER, false, AHEAD>), grid, dim3(NT * G), 0, stream, a);
     if (hipGetLastError() != hipSuccess) return MISGEMM_LAUNCH_FAILED;
     if (a.partials == nullptr) return MISGEMM_SUCCESS;
     hipLaunchKernelGGL(sum_partials, dim3((unsigned)((a.cols + 15) / 16)), dim3(256), 0, stream, a);
@@ -464,17 +532,21 @@ template <class T, class TW, int W, int G, int PER> int launch_back_rows(BackArg
 }
 
 template <class T, class TW> int launch_back(BackArgs a, hipStream_t stream) {
-    const bool in_registers = a.cols <= 16384;
+    static_assert(size_t(kGroups) * 16384 <= misgemm_workspace::kFloats, "partial rows fit the workspace");
+    const bool in_registers = a.cols >= 8 && a.cols <= 16384 && a.rows > 0;
     if (a.dweight != nullptr) {
-        float *partials = nullptr;
         int *counters = nullptr;
-        static_assert(size_t(kGroups) * 16384 <= misgemm_workspace::kFloats, "partial rows fit the workspace");
-        if (in_registers && a.rows > 0 && misgemm_workspace::get(stream, &partials, &counters)) {
-            a.partials = partials;
-        } else {
-            // Before dx is written: it may be dy.
-            hipLaunchKernelGGL((weight_grad<T>), dim3((unsigned)((a.cols + 63) / 64)), dim3(256), 0, stream, a);
+        const bool partial = in_registers && !few_rows(a) && misgemm_workspace::get(stream, &a.partials, &counters);
+        // Workgroups that read dy for the weight's gradient do not go with
+        // others that write dx there: they come first then, with the same sums.
+        if (!partial && (!in_registers || a.dx == a.dy)) {
+            const dim3 grid((unsigned)((a.cols + 63) / 64));
+            if (a.cols > 8192)
+                hipLaunchKernelGGL((weight_grad<T, 1024>), grid, dim3(1024), 0, stream, a);
+            else
+                hipLaunchKernelGGL((weight_grad<T, 512>), grid, dim3(512), 0, stream, a);
             if (hipGetLastError() != hipSuccess) return MISGEMM_LAUNCH_FAILED;
+            a.dweight = nullptr;
         }
     }
     if (a.rows == 0) return MISGEMM_SUCCESS;
@@ -483,12 +555,16 @@ template <class T, class TW> int launch_back(BackArgs a, hipStream_t stream) {
         hipLaunchKernelGGL((rmsnorm_back_long<T, TW>), grid, dim3(64 * kMaxWaves), 0, stream, a);
         return launched();
     }
-    if (a.cols <= 512) return launch_back_rows<T, TW, 1, 8, 1>(a, stream);
-    if (a.cols <= 1024) return launch_back_rows<T, TW, 2, 4, 1>(a, stream);
-    if (a.cols <= 2048) return launch_back_rows<T, TW, 4, 2, 1>(a, stream);
-    if (a.cols <= 4096) return launch_back_rows<T, TW, 8, 1, 1>(a, stream);
-    if (a.cols <= 8192) return launch_back_rows<T, TW, 8, 1, 2>(a, stream);
-    return launch_back_rows<T, TW, 16, 1, 2>(a, stream);
+    switch (back_threads(a.cols)) {
+        case 16: return launch_back_rows<T, TW, 16, 1>(a, stream);
+        case 32: return launch_back_rows<T, TW, 32, 1>(a, stream);
+        case 64: return launch_back_rows<T, TW, 64, 1>(a, stream);
+        case 128: return launch_back_rows<T, TW, 128, 1>(a, stream);
+        case 256: return launch_back_rows<T, TW, 256, 1>(a, stream);
+        case 512:
+            return a.cols <= 4096 ? launch_back_rows<T, TW, 512, 1>(a, stream) : launch_back_rows<T, TW, 512, 2>(a, stream);
+        default: return launch_back_rows<T, TW, 1024, 2>(a, stream);
+    }
 }
 
 }  // namespace

@@ -140,9 +140,10 @@ int mi_rmsnorm(int type, int wtype, int rows, int cols, const void *x, int ldx,
  *                      dx may be dh or dy itself.
  *   dweight            cols floats, or NULL: not wanted. beta == 0: not read.
  * rows == 0: dweight <- beta * dweight. cols == 0: nothing is done. The sum
- * over rows is split over workgroups whose partial sums go through the
- * stream's workspace (as in mi_sgemm) and are added in a fixed order; where
- * there is none, one workgroup sums all rows of its columns.
+ * over many rows is split over workgroups whose partial sums go through the
+ * stream's workspace (as in mi_sgemm) and are added in a fixed order; for few
+ * rows, and where there is no workspace, one workgroup sums all rows of its
+ * columns, in the same launch.
  */
 int mi_rmsnorm_backward(int type, int wtype, int rows, int cols, const void *dy, int lddy,
                         const void *h, int ldh, const void *weight, const float *rstd,
