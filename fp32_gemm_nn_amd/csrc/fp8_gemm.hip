@@ -66,48 +66,52 @@ template <int FA, int FB> __global__ __launch_bounds__(256) void fp8_short(GemmA
 }
 
 // The kernel that is expected to be fastest: 0 to 5 are fp8_direct.hip's tile
-// shapes, 16 to 18 those of fp8_tile.hip.
+// shapes, 16 to 20 those of fp8_tile.hip.
 //
 // A product's time in us is taken to be first + round * (rounds - 1) + step *
 // rounds * steps, where a round is 256 workgroups (one for each CU) and a step
 // is a block of k for each of a workgroup's waves that split k. The constants
-// are fitted to the measured times of all kernels on 78 shapes (M, N and K
-// from 1, 64 and 64 to 8192, all types of C and kinds of scales), which they
-// reproduce to 8-17%; the kernel picked was within 1.2% of the fastest on
-// average, and 24% at worst.
+// are fitted to the measured times of all kernels on 356 shapes (M, N and K
+// from 1, 64 and 64 to 8192, all types of C, kinds of scales and alignments),
+// which they reproduce to 8-18%; the kernel picked was 1.8% slower than the
+// fastest on average, and 43% at worst (256 x 6232 x 3248, rows 4 bytes aligned).
 struct Cost {
     int kernel, bm, bn, waves;
     struct {
         float first, round, step;
-    } fit[2];   // C of 16 bits; of 32, with BF16 products
+    } fit[2][2];   // C of 16 bits; of 32, with BF16 products. Rows 16 bytes aligned; not
 };
 constexpr Cost kCosts[] = {
-    {0, 16, 16, 16, {{2.4f, 0.40f, 0.88f}, {2.25f, 0.67f, 0.97f}}},
-    {1, 16, 32, 8, {{2.7f, 0.41f, 0.56f}, {2.5f, 0.96f, 0.79f}}},
-    {2, 32, 32, 8, {{2.8f, 0.48f, 0.78f}, {2.7f, 1.12f, 0.95f}}},
-    {3, 64, 32, 8, {{2.65f, 1.55f, 1.47f}, {2.8f, 2.06f, 1.60f}}},
-    {4, 64, 32, 4, {{3.4f, 0.41f, 0.69f}, {3.4f, 0.64f, 0.96f}}},
-    {5, 64, 64, 8, {{2.5f, 2.65f, 2.09f}, {}}},
-    {16, 128, 128, 1, {{4.7f, 2.24f, 0.72f}, {5.5f, 3.96f, 1.27f}}},
-    {17, 128, 128, 1, {{4.8f, 2.53f, 0.55f}, {5.8f, 3.47f, 0.95f}}},
-    {18, 256, 256, 1, {{6.7f, 12.5f, 1.42f}, {}}},
+    {0, 16, 16, 16, {{{2.40f, 0.66f, 0.83f}, {1.68f, 0, 1.67f}}, {{2.26f, 0.46f, 1.01f}, {1.65f, 0, 1.69f}}}},
+    {1, 16, 32, 8, {{{2.50f, 0.19f, 0.66f}, {2.21f, 0, 1.14f}}, {{2.44f, 0.77f, 0.83f}, {2.00f, 0.24f, 1.34f}}}},
+    {2, 32, 32, 8, {{{2.55f, 0.23f, 0.85f}, {2.33f, 0, 1.39f}}, {{2.67f, 0.85f, 1.03f}, {2.14f, 0.37f, 1.76f}}}},
+    {3, 64, 32, 8, {{{2.37f, 1.33f, 1.58f}, {2.07f, 0.82f, 2.33f}}, {{2.60f, 1.59f, 1.88f}, {1.97f, 1.29f, 2.82f}}}},
+    {4, 64, 32, 4, {{{3.13f, 0.20f, 0.78f}, {3.18f, 0, 1.17f}}, {{3.27f, 0.41f, 0.98f}, {3.27f, 0.42f, 1.38f}}}},
+    {5, 64, 64, 8, {{{2.96f, 2.59f, 1.96f}, {2.49f, 1.42f, 2.99f}}, {}}},
+    {16, 128, 128, 1, {{{}, {5.21f, 1.55f, 0.98f}}, {{}, {6.53f, 2.46f, 1.31f}}}},
+    {17, 64, 128, 1, {{{}, {3.91f, 0.13f, 0.80f}}, {{}, {4.79f, 1.17f, 1.00f}}}},
+    {18, 64, 128, 1, {{{4.22f, 0.94f, 0.40f}, {}}, {{4.46f, 0.82f, 0.70f}, {}}}},
+    {19, 128, 128, 1, {{{5.36f, 2.31f, 0.56f}, {}}, {{6.06f, 3.20f, 0.89f}, {}}}},
+    {20, 256, 256, 1, {{{9.12f, 8.79f, 1.57f}, {}}, {}}},
 };
-constexpr float kSplitCost = 7.0f;   // exchanging partial tiles
+constexpr float kSplitCost = 8.0f;   // exchanging partial tiles
 
 int pick(const GemmArgs &g, bool rows) {
-    const bool exact = g.ctype == MI_F32, direct = g.lda < 1 << 26 && g.ldb < 1 << 26;
+    const bool exact = g.ctype == MI_F32, near = g.lda < 1 << 24 && g.ldb < 1 << 24;
+    const bool direct = g.lda < 1 << 26 && g.ldb < 1 << 26;
     int best = 16;
     float least = 3e38f;
     for (const Cost &c : kCosts) {
         const long long tiles = (g.M + c.bm - 1LL) / c.bm * ((g.N + c.bn - 1LL) / c.bn);
         if (c.kernel < 16 && (!direct || tiles * 64 * c.waves >= 1LL << 32)) continue;
         if (c.kernel == 5 && (exact || rows)) continue;   // does not fit the registers
-        if (c.kernel == 18 && exact) continue;
-        if (c.kernel >= 16 && (c.kernel > 16) != g.direct) continue;
-        const int splits = c.kernel == 16 || c.kernel == 17 ? splits_of(tiles, blocks(g.K)) : 1;
+        if (c.kernel == 20 && exact) continue;            // nor that
+        if (c.kernel >= 16 && (c.kernel > 17) != g.direct) continue;
+        if (c.kernel == 17 && !near) continue;
+        const int splits = c.kernel == 16 || c.kernel == 19 ? splits_of(tiles, blocks(g.K)) : 1;
         const float rounds = (float)((tiles * splits + kNumCus - 1) / kNumCus);
         const float steps = (float)((blocks(g.K) + c.waves * splits - 1) / (c.waves * splits));
-        const auto &f = c.fit[exact];
+        const auto &f = c.fit[exact][!g.direct];
         const float us = f.first + f.round * (rounds - 1) + f.step * rounds * steps + (splits > 1 ? kSplitCost : 0.0f);
         if (us < least) {
             least = us;

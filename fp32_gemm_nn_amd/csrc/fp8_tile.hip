@@ -12,7 +12,9 @@
 // what 128 x 128 tiles read from L2 and LDS: 8192 x 8192 x 4096 to BF16 takes
 // 241 us (2.28 PFLOP/s) in the former and 294 us in the latter, two workgroups
 // of which share a CU. Below 256 tiles of 256 x 256 CUs stay empty, and the
-// smaller ones win (2048 x 4096 x 1024: 14.9 us and 20.6 us). What bounds it:
+// smaller ones win (2048 x 4096 x 1024: 14.9 us and 20.6 us); 64 x 128 tiles
+// fill the gap to fp8_direct.hip (331 x 5752 x 352 with row scales: 7.1 us,
+// 7.7 in tiles of 128 x 128, 10.5 there). What bounds it:
 // the matrix cores are busy 57% of the time; the operands' way from L2 to LDS
 // alone takes 220 us (measured with the products left out), the products alone
 // 217 us. FP32 results (BF16 products, half the rate) are nearer to the matrix
@@ -60,7 +62,23 @@ template <int ROWS, int NT> struct Stage {
         for (int j = 0; j < PER; ++j)
             load_lds<16>(src, at[j], lds + 16 * NT * j);
     }
-    // Any block and alignment, in two steps. A chunk that passes K (K >= 16) is
+    // The same of any block and alignment, in two steps, for leading dimensions
+    // below 2^24. A chunk that passes K (K >= 16) is read as the 16 bytes before
+    // K and moved on its way to LDS. `at` are offsets of whole rows; `src` is 16
+    // bytes low, to keep offsets positive.
+    static __device__ __forceinline__ void rows_at(uint32_t (&at)[PER], int ld, int rows, int tid) {
+#pragma unroll
+        for (int j = 0; j < PER; ++j) at[j] = min(row(tid, j), rows - 1) * (uint32_t)ld;
+    }
+    static __device__ __forceinline__ void fetch_near(i32x4 (&w)[PER], const uint8_t *src, const uint32_t (&at)[PER],
+                                                      int left, int tid) {
+        static_assert(NT / 8 % 8 == 0, "a thread's chunks are in one place of their rows");
+        const uint32_t off = 16 + min(16 * chunk(tid, 0), left - 16);
+#pragma unroll
+        for (int j = 0; j < PER; ++j)
+            w[j] = *reinterpret_cast<const words16 *>(src - 16 + (at[j] + off));
+    }
+    // The same for any leading dimension. A chunk that passes K (K >= 16) is
     // read as the 16 bytes before K and moved on its way to LDS.
     static __device__ __forceinline__ void fetch(i32x4 (&w)[PER], const uint8_t *src, long long ld, int rows, int k0,
                                                  int K, int tid) {
@@ -69,11 +87,13 @@ template <int ROWS, int NT> struct Stage {
             w[j] = *reinterpret_cast<const words16 *>(src + min(row(tid, j), rows - 1) * ld +
                                                       min(k0 + 16 * chunk(tid, j), K - 16));
     }
-    static __device__ __forceinline__ void write(i32x4 (&w)[PER], int k0, int K, int tid, uint8_t *lds) {
+    static __device__ __forceinline__ void settle(i32x4 (&w)[PER], int k0, int K, int tid) {
         if (k0 + kBlock > K) {
 #pragma unroll
             for (int j = 0; j < PER; ++j) w[j] = shifted(w[j], k0 + 16 * chunk(tid, j) + 16 - K);
         }
+    }
+    static __device__ __forceinline__ void write(const i32x4 (&w)[PER], int tid, uint8_t *lds) {
 #pragma unroll
         for (int j = 0; j < PER; ++j) *reinterpret_cast<i32x4 *>(lds + 16 * (tid + NT * j)) = w[j];
     }
@@ -105,12 +125,14 @@ __device__ __forceinline__ void meet() {
     asm volatile("" ::: "memory");
 }
 
-// ANY: operands of any alignment and leading dimension, which go through
-// registers on their way to LDS.
-template <int BM, int BN, int WM, int WN, int FA, int FB, bool ROWB, bool EXACT, bool ANY>
-__global__ __launch_bounds__(64 * WM * WN, ANY && EXACT && ROWB ? 1 : 2) void fp8_tile(GemmArgs g) {
+enum Way { DIRECT, STAGED, FAR };   // operands to LDS: without registers, through them, with any leading dimension
+
+template <int BM, int BN, int WM, int WN, int FA, int FB, bool ROWB, bool EXACT, Way WAY>
+__global__ __launch_bounds__(64 * WM * WN, WAY == FAR && EXACT && ROWB ? 1 : 2) void fp8_tile(GemmArgs g) {
+    constexpr bool ANY = WAY != DIRECT;
     constexpr int NT = 64 * WM * WN, TM = BM / WM, TN = BN / WN, MI = TM / 16, NI = TN / 16;
-    static_assert(TN == 64 && MI % 4 == 0, "a wave's columns share a block, its outputs leave 64 x 64 at a time");
+    constexpr int ROWS = MI < 4 ? MI : 4;   // sixteens of rows that leave at a time
+    static_assert(TN == 64 && MI % ROWS == 0, "a wave's columns share a block, and leave as whole rows");
     using StageA = Stage<BM, NT>;
     using StageB = Stage<BN, NT>;
     constexpr int OPERANDS = (BM + BN) * kBlock, SB = ROWB ? 4 * NI : 1;
@@ -159,9 +181,12 @@ __global__ __launch_bounds__(64 * WM * WN, ANY && EXACT && ROWB ? 1 : 2) void fp
     };
 
     uint32_t from_a[StageA::PER], from_b[StageB::PER];
-    if constexpr (!ANY) {
+    if constexpr (WAY == DIRECT) {
         StageA::offsets(from_a, (int)g.lda, g.M - m0, tid);
         StageB::offsets(from_b, (int)g.ldb, g.N - n0, tid);
+    } else if constexpr (WAY == STAGED) {
+        StageA::rows_at(from_a, (int)g.lda, g.M - m0, tid);
+        StageB::rows_at(from_b, (int)g.ldb, g.N - n0, tid);
     }
     auto copy = [&](int kb, int buf) {
         // Hides that kb counts a loop: known as such, each load would get a
@@ -176,12 +201,19 @@ __global__ __launch_bounds__(64 * WM * WN, ANY && EXACT && ROWB ? 1 : 2) void fp
     };
     auto fetch = [&](Chunks &w, int kb) {
         asm("" : "+s"(kb));
+        if constexpr (WAY == STAGED) {
+            StageA::fetch_near(w.a, A0 + (long long)kb * kBlock, from_a, g.K - kb * kBlock, tid);
+            StageB::fetch_near(w.b, B0 + (long long)kb * kBlock, from_b, g.K - kb * kBlock, tid);
+            return;
+        }
         StageA::fetch(w.a, A0, g.lda, g.M - m0, kb * kBlock, g.K, tid);
         StageB::fetch(w.b, B0, g.ldb, g.N - n0, kb * kBlock, g.K, tid);
     };
     auto write = [&](Chunks &w, int kb, int buf) {
-        StageA::write(w.a, kb * kBlock, g.K, tid, lds[buf]);
-        StageB::write(w.b, kb * kBlock, g.K, tid, lds[buf] + BM * kBlock);
+        StageA::settle(w.a, kb * kBlock, g.K, tid);
+        StageB::settle(w.b, kb * kBlock, g.K, tid);
+        StageA::write(w.a, tid, lds[buf]);
+        StageB::write(w.b, tid, lds[buf] + BM * kBlock);
         copy_scales(kb, lds[buf]);
     };
 
@@ -341,22 +373,22 @@ __global__ __launch_bounds__(64 * WM * WN, ANY && EXACT && ROWB ? 1 : 2) void fp
     }
 
     // A lane holds four neighbouring outputs of a row; stored like that, 16
-    // rows at once, they would leave in pieces of 16 bytes. So 64 x 64 outputs
-    // at a time turn in LDS, each wave's in its own, and leave as whole rows.
+    // rows at once, they would leave in pieces of 16 bytes. So up to 64 x 64
+    // outputs at a time turn in LDS, each wave's in its own, and leave as whole rows.
     // Chunk c of row r is at c ^ (r & 15).
     meet();
-    f32x4 *own = reinterpret_cast<f32x4 *>(lds) + wave * 64 * 16;
+    f32x4 *own = reinterpret_cast<f32x4 *>(lds) + wave * ROWS * 256;
     const int m1 = m0 + wm * TM, n1 = n0 + wn * TN;
 #pragma unroll
-    for (int a0 = 0; a0 < MI; a0 += 4) {
+    for (int a0 = 0; a0 < MI; a0 += ROWS) {
 #pragma unroll
-        for (int a = 0; a < 4; ++a)
+        for (int a = 0; a < ROWS; ++a)
 #pragma unroll
             for (int b = 0; b < NI; ++b) own[(16 * a + i) * 16 + ((4 * b + grp) ^ i)] = acc[a0 + a][b];
         asm volatile("" ::: "memory");
         constexpr int N = EXACT ? 4 : 8, LANES = 64 / N;   // outputs of a lane, lanes of a row
 #pragma unroll 4
-        for (int r0 = 0; r0 < 64; r0 += 64 / LANES) {
+        for (int r0 = 0; r0 < 16 * ROWS; r0 += 64 / LANES) {
             const int r = r0 + lane / LANES, c = lane % LANES * (N / 4);
             float v[N];
 #pragma unroll
@@ -371,7 +403,7 @@ __global__ __launch_bounds__(64 * WM * WN, ANY && EXACT && ROWB ? 1 : 2) void fp
     }
 }
 
-template <int BM, int BN, int WM, int WN, int FA, int FB, bool ROWB, bool EXACT, bool ANY>
+template <int BM, int BN, int WM, int WN, int FA, int FB, bool ROWB, bool EXACT, Way WAY>
 int launch_tile(GemmArgs &g, bool split, hipStream_t stream) {
     g.tiles_m = (g.M + BM - 1) / BM;
     g.tiles_n = (g.N + BN - 1) / BN;
@@ -382,17 +414,25 @@ int launch_tile(GemmArgs &g, bool split, hipStream_t stream) {
                   2 * kNumCus <= misgemm_workspace::kCounters, "partial tiles fit the workspace");
     if (g.splits > 1 && !misgemm_workspace::get(stream, &g.ws, &g.counters)) g.splits = 1;
     g.kb_per_split = (kblocks + g.splits - 1) / g.splits;
-    hipLaunchKernelGGL((fp8_tile<BM, BN, WM, WN, FA, FB, ROWB, EXACT, ANY>), dim3((unsigned)(tiles * g.splits)),
+    hipLaunchKernelGGL((fp8_tile<BM, BN, WM, WN, FA, FB, ROWB, EXACT, WAY>), dim3((unsigned)(tiles * g.splits)),
                        dim3(64 * WM * WN), 0, stream, g);
     return launched();
 }
 
 template <int FA, int FB, bool ROWB, bool EXACT> int launch(int shape, GemmArgs &g, hipStream_t stream) {
-    if (shape == 0) return launch_tile<128, 128, 2, 2, FA, FB, ROWB, EXACT, true>(g, true, stream);
-    // Widened operands of 128 x 64 outputs do not fit a wave's registers.
-    if constexpr (!EXACT)
-        if (shape == 2) return launch_tile<256, 256, 2, 4, FA, FB, ROWB, EXACT, false>(g, false, stream);
-    return launch_tile<128, 128, 2, 2, FA, FB, ROWB, EXACT, false>(g, true, stream);
+    const bool near = g.lda < 1 << 24 && g.ldb < 1 << 24;
+    switch (shape) {
+        case 0:
+            if (near) return launch_tile<128, 128, 2, 2, FA, FB, ROWB, EXACT, STAGED>(g, true, stream);
+            return launch_tile<128, 128, 2, 2, FA, FB, ROWB, EXACT, FAR>(g, true, stream);
+        case 1: return launch_tile<64, 128, 2, 2, FA, FB, ROWB, EXACT, STAGED>(g, false, stream);
+        case 2: return launch_tile<64, 128, 2, 2, FA, FB, ROWB, EXACT, DIRECT>(g, false, stream);
+        case 3: return launch_tile<128, 128, 2, 2, FA, FB, ROWB, EXACT, DIRECT>(g, true, stream);
+        default:
+            // Widened operands of 128 x 64 outputs do not fit a wave's registers.
+            if constexpr (!EXACT) return launch_tile<256, 256, 2, 4, FA, FB, ROWB, EXACT, DIRECT>(g, false, stream);
+            return MISGEMM_LAUNCH_FAILED;
+    }
 }
 
 template <int FA, int FB> int launch(bool rows, int shape, GemmArgs &g, hipStream_t stream) {

@@ -46,7 +46,8 @@ def powers(g, *shape):
 SIZES = [(1, 700, 8192), (16, 900, 130), (20, 4100, 300), (64, 1024, 2048), (100, 3000, 1000), (300, 1000, 1030),
          (500, 2050, 900), (700, 1400, 640), (1000, 1300, 700), (1500, 1500, 1600), (600, 3000, 3000),
          (2500, 2600, 400), (3000, 3000, 300), (2100, 4100, 260), (4096, 4096, 256), (1024, 2048, 8192),
-         (257, 8000, 4100), (3001, 2999, 16), (2048, 2048, 2048)]
+         (257, 8000, 4100), (3001, 2999, 16), (2048, 2048, 2048), (331, 5752, 352), (136, 7840, 2048),
+         (418, 3648, 2580)]
 
 
 @pytest.mark.parametrize("pad", [0, 3])
