@@ -19,8 +19,9 @@
 // (1.9e-8 off) at half the rate.
 //
 // The product's first operand is B and its second A: a lane then holds
-// outputs of one row of A (one sA) at neighbouring columns. Which 32 values of k a lane group feeds does not matter as
-// long as it is the same for both operands.
+// outputs of one row of A (one sA) at neighbouring columns. Which 32 values of
+// k a lane group feeds does not matter as long as it is the same for both
+// operands.
 
 #include "fp8_gemm.h"
 
@@ -105,7 +106,7 @@ int pick(const GemmArgs &g, bool rows) {
         const long long tiles = (g.M + c.bm - 1LL) / c.bm * ((g.N + c.bn - 1LL) / c.bn);
         if (c.kernel < 16 && (!direct || tiles * 64 * c.waves >= 1LL << 32)) continue;
         if (c.kernel == 5 && (exact || rows)) continue;   // does not fit the registers
-        if (c.kernel == 20 && exact) continue;            // nor that
+        if (c.kernel == 20 && (exact || g.ldsb >= 1 << 28)) continue;   // nor that; 32-bit offsets of scales
         if (c.kernel >= 16 && (c.kernel > 17) != g.direct) continue;
         if (c.kernel == 17 && !near) continue;
         const int splits = c.kernel == 16 || c.kernel == 19 ? splits_of(tiles, blocks(g.K)) : 1;
@@ -179,8 +180,9 @@ extern "C" int mi_fp8_gemm(int atype, int btype, int block, int ctype, int M, in
     const bool rows = block == MI_BLOCK_ROW;
     if (K < 16) {
         const dim3 grid((unsigned)((N + 255LL) / 256), (unsigned)(M < 65535 ? M : 65535));
-        const auto kernel = atype == MI_E4M3 ? (btype == MI_E4M3 ? fp8_short<MI_E4M3, MI_E4M3> : fp8_short<MI_E4M3, MI_E5M2>)
-                                             : (btype == MI_E4M3 ? fp8_short<MI_E5M2, MI_E4M3> : fp8_short<MI_E5M2, MI_E5M2>);
+        const auto kernel = atype == MI_E4M3
+                                ? (btype == MI_E4M3 ? fp8_short<MI_E4M3, MI_E4M3> : fp8_short<MI_E4M3, MI_E5M2>)
+                                : (btype == MI_E4M3 ? fp8_short<MI_E5M2, MI_E4M3> : fp8_short<MI_E5M2, MI_E5M2>);
         hipLaunchKernelGGL(kernel, grid, dim3(256), 0, stream, g, rows);
         return launched();
     }

@@ -43,7 +43,8 @@ template <int BYTES> __device__ __forceinline__ void load_lds(const void *base, 
 
 // One operand's 128 bytes of k for ROWS rows in LDS: rows of eight 16-byte
 // chunks, chunk c of row r at position c ^ swz(r), so that the 16 rows a
-// fragment read touches spread over all banks. Rows past the matrix repeat its last one: their outputs are not stored.
+// fragment read touches spread over all banks. Rows past the matrix repeat its
+// last one: their outputs are not stored.
 template <int ROWS, int NT> struct Stage {
     static constexpr int PER = ROWS * 8 / NT;
     static_assert(PER * NT == ROWS * 8 && NT % 64 == 0, "whole chunks per thread");

@@ -118,7 +118,8 @@ __global__ __launch_bounds__(NT *G) void rmsnorm(NormArgs a) {
             for (int j = 0; j < 8; ++j) {
                 h[p][j] = static_cast<float>(x[p].v[j]);
                 // Rounded to T as it is kept.
-                if (a.res != nullptr) h[p][j] = static_cast<float>(static_cast<T>(h[p][j] + static_cast<float>(r[p].v[j])));
+                if (a.res != nullptr)
+                    h[p][j] = static_cast<float>(static_cast<T>(h[p][j] + static_cast<float>(r[p].v[j])));
                 sum = fmaf(h[p][j], h[p][j], sum);
             }
         }
@@ -562,7 +563,8 @@ template <class T, class TW> int launch_back(BackArgs a, hipStream_t stream) {
         case 128: return launch_back_rows<T, TW, 128, 1>(a, stream);
         case 256: return launch_back_rows<T, TW, 256, 1>(a, stream);
         case 512:
-            return a.cols <= 4096 ? launch_back_rows<T, TW, 512, 1>(a, stream) : launch_back_rows<T, TW, 512, 2>(a, stream);
+            return a.cols <= 4096 ? launch_back_rows<T, TW, 512, 1>(a, stream)
+                                  : launch_back_rows<T, TW, 512, 2>(a, stream);
         default: return launch_back_rows<T, TW, 1024, 2>(a, stream);
     }
 }
