@@ -29,6 +29,7 @@ Quantize call_quantize = nullptr;
 Norm call_norm = nullptr;
 Backward call_backward = nullptr;
 PyObject *raw_stream = nullptr;   // device index -> address of torch's current stream
+PyObject *exchange = nullptr;     // makes a device index current, and returns the one before
 
 constexpr int64_t kMost = 0x7fffffff;
 
@@ -103,13 +104,15 @@ bool number(PyObject *o, float &f) {
     f = static_cast<float>(d);
     return true;
 }
+// `f` of a device index.
+PyObject *of_device(PyObject *f, int device) {
+    PyObject *index = PyLong_FromLong(device);
+    PyObject *value = index == nullptr ? nullptr : PyObject_CallOneArg(f, index);
+    Py_XDECREF(index);
+    return value;
+}
 bool stream_of(PyObject *o, int device, void **stream) {
-    PyObject *value = o;
-    if (o == Py_None) {
-        PyObject *index = PyLong_FromLong(device);
-        value = index == nullptr ? nullptr : PyObject_CallOneArg(raw_stream, index);
-        Py_XDECREF(index);
-    }
+    PyObject *value = o == Py_None ? of_device(raw_stream, device) : o;
     const bool ok = value != nullptr && PyLong_Check(value);
     if (ok) *stream = PyLong_AsVoidPtr(value);
     if (o == Py_None) Py_XDECREF(value);
@@ -119,6 +122,24 @@ bool stream_of(PyObject *o, int device, void **stream) {
     }
     return true;
 }
+
+// The tensors' device is current while this lives: stream 0, torch's default
+// one on every device, is the current device's.
+struct OnDevice {
+    int before = -1, device;
+    explicit OnDevice(int device) : device(device) {
+        PyObject *value = of_device(exchange, device);
+        if (value != nullptr && PyLong_Check(value)) before = (int)PyLong_AsLong(value);
+        Py_XDECREF(value);
+        PyErr_Clear();
+    }
+    bool ok() const { return before >= 0; }
+    ~OnDevice() {
+        if (before < 0 || before == device) return;
+        Py_XDECREF(of_device(exchange, before));
+        PyErr_Clear();
+    }
+};
 
 // Runs `f`, which fills a status and says whether it made the call.
 template <class F> PyObject *taken(F f) {
@@ -148,6 +169,8 @@ PyObject *gemm(PyObject *, PyObject *const *a, Py_ssize_t n) {
         if (!read_table(a[4], B.rows, B.cols, block == 1, A.device, sb)) return false;
         if (!C.apart(A) || !C.apart(B) || !C.apart(sa) || !C.apart(sb)) return false;
         if (!number(a[0], alpha) || !number(a[5], beta) || !stream_of(a[8], A.device, &stream)) return false;
+        const OnDevice on(A.device);
+        if (!on.ok()) return false;
         Py_BEGIN_ALLOW_THREADS
         status = call_gemm(A.type, B.type, block, C.type, A.rows, B.rows, A.cols, alpha, A.ptr, A.ld,
                            reinterpret_cast<const float *>(sa.ptr), sa.ld, B.ptr, B.ld,
@@ -179,6 +202,8 @@ PyObject *quantize(PyObject *, PyObject *const *a, Py_ssize_t n) {
             if (one && (!qt.apart(q) || !qt.apart(s) || !st.apart(q) || !st.apart(s))) return false;
         }
         if (!stream_of(a[6], x.device, &stream)) return false;
+        const OnDevice on(x.device);
+        if (!on.ok()) return false;
         Py_BEGIN_ALLOW_THREADS
         status = call_quantize(x.type, x.rows, x.cols, x.ptr, x.ld, one ? q.type : qt.type, block, q.ptr, q.ld,
                                reinterpret_cast<float *>(s.ptr), s.ld, qt.ptr, qt.ld,
@@ -216,6 +241,8 @@ PyObject *rmsnorm(PyObject *, PyObject *const *a, Py_ssize_t n) {
                 if (!out[i].apart(out[j])) return false;
         }
         if (!number(a[2], eps) || !stream_of(a[9], x.device, &stream)) return false;
+        const OnDevice on(x.device);
+        if (!on.ok()) return false;
         Py_BEGIN_ALLOW_THREADS
         status = call_norm(x.type, w.type, x.rows, x.cols, x.ptr, x.ld, r.ptr, r.ld, w.ptr, eps, out[0].ptr, out[0].ld,
                            out[1].ptr, out[1].ld, given(a[6]) ? out[2].type : 3, out[2].ptr, out[2].ld,
@@ -244,6 +271,8 @@ PyObject *rmsnorm_backward(PyObject *, PyObject *const *a, Py_ssize_t n) {
         if ((!dx.apart(dy) && !dx.same(dy)) || (!dx.apart(dh) && !dx.same(dh))) return false;
         if (!dw.apart(dy) || !dw.apart(h) || !dw.apart(w) || !dw.apart(rstd) || !dw.apart(dh)) return false;
         if (!number(a[7], beta) || !stream_of(a[8], dy.device, &stream)) return false;
+        const OnDevice on(dy.device);
+        if (!on.ok()) return false;
         Py_BEGIN_ALLOW_THREADS
         status = call_backward(dy.type, w.type, dy.rows, dy.cols, dy.ptr, dy.ld, h.ptr, h.ld, w.ptr,
                                reinterpret_cast<const float *>(rstd.ptr), dh.ptr, dh.ld, dx.ptr, dx.ld, beta,
@@ -254,11 +283,12 @@ PyObject *rmsnorm_backward(PyObject *, PyObject *const *a, Py_ssize_t n) {
 }
 
 // The addresses of mi_fp8_gemm, mi_fp8_quantize, mi_rmsnorm and
-// mi_rmsnorm_backward, and what gives a device's current stream.
+// mi_rmsnorm_backward, what gives a device's current stream, and what makes a
+// device current.
 PyObject *bind(PyObject *, PyObject *const *a, Py_ssize_t n) {
     void *at[4];
-    if (n != 5) {
-        PyErr_SetString(PyExc_TypeError, "bind takes four addresses and a function");
+    if (n != 6) {
+        PyErr_SetString(PyExc_TypeError, "bind takes four addresses and two functions");
         return nullptr;
     }
     for (int i = 0; i < 4; ++i) {
@@ -272,6 +302,9 @@ PyObject *bind(PyObject *, PyObject *const *a, Py_ssize_t n) {
     Py_INCREF(a[4]);
     Py_XDECREF(raw_stream);
     raw_stream = a[4];
+    Py_INCREF(a[5]);
+    Py_XDECREF(exchange);
+    exchange = a[5];
     Py_RETURN_NONE;
 }
 

@@ -3,7 +3,8 @@
 Functions with the C names (``include/misgemm_fp8.h``) take raw device
 pointers (ints) and return the C status code. The tensor forms beside them
 check shapes, types, devices and overlap, enqueue on ``stream`` (default: the
-current torch stream of the tensors' device) and raise on an error. Outputs
+current torch stream of the tensors' device, which is current for the call:
+stream 0 is its default stream) and raise on an error. Outputs
 are tensors of the caller's, written in place; nothing is computed here.
 What is plainly right goes through a C++ binding in about a microsecond; the
 checks below name what is not, and decide the rest (memory that interleaves).
@@ -49,7 +50,8 @@ def _load_native():
     loader.exec_module(module)
     address = [ctypes.cast(f, ctypes.c_void_p).value
                for f in (lib.mi_fp8_gemm, lib.mi_fp8_quantize, lib.mi_rmsnorm, lib.mi_rmsnorm_backward)]
-    module.bind(*address, getattr(torch._C, "_cuda_getCurrentRawStream", lambda index: None))
+    module.bind(*address, getattr(torch._C, "_cuda_getCurrentRawStream", lambda index: None),
+                getattr(torch._C, "_cuda_exchangeDevice", lambda index: None))
     _native = module
     return module
 
@@ -145,8 +147,10 @@ def _apart(outs, ins):
                 raise ValueError(f"{name} must not overlap {other}")
 
 
-def _stream(stream, device) -> int:
-    return torch.cuda.current_stream(device).cuda_stream if stream is None else stream
+def _enqueue(entry, device, stream, *args) -> int:
+    """Call a C function on a stream with its device current: stream 0 (torch's default) is the current device's."""
+    with torch.cuda.device(device):
+        return entry(*args, torch.cuda.current_stream(device).cuda_stream if stream is None else stream)
 
 
 def _on_device(name, t):
@@ -212,8 +216,8 @@ def fp8_quantize(x, q=None, scale=None, qt=None, scale_t=None, block: str = "row
         args += [o.ptr, o.ld, z.ptr, z.ld]
         given += [t, s]
     _apart(outs, ins)
-    _raise(mi_fp8_quantize(_REAL[x.dtype], rows, cols, a.ptr, max(a.ld, cols), _F8[given[0].dtype], _BLOCK[block],
-                           *args, _stream(stream, dev)), "mi_fp8_quantize")
+    _raise(_enqueue(mi_fp8_quantize, dev, stream, _REAL[x.dtype], rows, cols, a.ptr, max(a.ld, cols),
+                    _F8[given[0].dtype], _BLOCK[block], *args), "mi_fp8_quantize")
     return tuple(given)
 
 
@@ -236,8 +240,8 @@ def fp8_gemm(alpha: float, A, scale_a, B, scale_b, beta: float, C, block: str = 
     sb = _Arg("scale_b", scale_b, _table(N, K, block), (torch.float32,), dev)
     c = _Arg("C", C, (M, N), _REAL, dev)
     _apart([("C", c, C.element_size())], [("A", a, 1), ("scale_a", sa, 4), ("B", b, 1), ("scale_b", sb, 4)])
-    _raise(mi_fp8_gemm(_F8[A.dtype], _F8[B.dtype], _BLOCK[block], _REAL[C.dtype], M, N, K, alpha, a.ptr, a.ld, sa.ptr,
-                       sa.ld, b.ptr, b.ld, sb.ptr, sb.ld, beta, c.ptr, c.ld, _stream(stream, dev)), "mi_fp8_gemm")
+    _raise(_enqueue(mi_fp8_gemm, dev, stream, _F8[A.dtype], _F8[B.dtype], _BLOCK[block], _REAL[C.dtype], M, N, K, alpha,
+                    a.ptr, a.ld, sa.ptr, sa.ld, b.ptr, b.ld, sb.ptr, sb.ld, beta, c.ptr, c.ld), "mi_fp8_gemm")
     return C
 
 
@@ -284,9 +288,9 @@ def rmsnorm(x, weight, eps: float, residual=None, h=None, y=None, q=None, scale=
     for name, o, s in outs:
         _apart([(name, o, s)], [i for i in ins if not (name == "h" and i[0] != "weight" and _same(o, i[1]))])
     _apart(outs, [])
-    _raise(mi_rmsnorm(_REAL[x.dtype], _REAL[weight.dtype], rows, cols, ax.ptr, max(ax.ld, cols), ptr["residual"],
-                      ld["residual"], aw.ptr, eps, ptr["h"], ld["h"], ptr["y"], ld["y"], *qa,
-                      0 if rstd is None else rstd.data_ptr(), _stream(stream, dev)), "mi_rmsnorm")
+    _raise(_enqueue(mi_rmsnorm, dev, stream, _REAL[x.dtype], _REAL[weight.dtype], rows, cols, ax.ptr, max(ax.ld, cols),
+                    ptr["residual"], ld["residual"], aw.ptr, eps, ptr["h"], ld["h"], ptr["y"], ld["y"], *qa,
+                    0 if rstd is None else rstd.data_ptr()), "mi_rmsnorm")
 
 
 def rmsnorm_backward(dy, h, weight, rstd, dx, dweight=None, dh=None, beta: float = 0.0, stream=None):
@@ -317,8 +321,7 @@ def rmsnorm_backward(dy, h, weight, rstd, dx, dweight=None, dh=None, beta: float
     _apart(outs[:1], [i for i in ins if not (i[0] in ("dy", "dh") and _same(adx, i[1]))])
     _apart(outs[1:], ins)
     _apart(outs, [])
-    _raise(mi_rmsnorm_backward(_REAL[dy.dtype], _REAL[weight.dtype], rows, cols, ady.ptr, max(ady.ld, cols), ah.ptr,
-                               max(ah.ld, cols), aw.ptr, ar.ptr, 0 if adh is None else adh.ptr,
-                               0 if adh is None else adh.ld, adx.ptr, max(adx.ld, cols), beta,
-                               0 if dweight is None else dweight.data_ptr(), _stream(stream, dev)),
-           "mi_rmsnorm_backward")
+    _raise(_enqueue(mi_rmsnorm_backward, dev, stream, _REAL[dy.dtype], _REAL[weight.dtype], rows, cols, ady.ptr,
+                    max(ady.ld, cols), ah.ptr, max(ah.ld, cols), aw.ptr, ar.ptr, 0 if adh is None else adh.ptr,
+                    0 if adh is None else adh.ld, adx.ptr, max(adx.ld, cols), beta,
+                    0 if dweight is None else dweight.data_ptr()), "mi_rmsnorm_backward")
