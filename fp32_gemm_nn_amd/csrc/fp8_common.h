@@ -88,7 +88,7 @@ template <class T, bool EVEN> struct Eight {
     }
     // After `fetch`, at the first use.
     __device__ __forceinline__ void settle(int col, int cols) {
-        const int over = max(col + 8 - cols, 0);
+        const int over = max(col - (cols - 8), 0);   // col + 8 may pass 2^31
         words w = __builtin_bit_cast(words, v);
         if constexpr (EVEN) {
 #pragma unroll

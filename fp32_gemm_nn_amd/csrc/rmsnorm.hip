@@ -455,7 +455,10 @@ __global__ __launch_bounds__(64 * kMaxWaves) void rmsnorm_back_long(BackArgs a) 
 
 // The weight's gradient alone.
 template <class T, int NT> __global__ __launch_bounds__(NT) void weight_grad(BackArgs a) {
-    grad_columns<T, NT>(a, blockIdx.x);
+    for (int block = blockIdx.x; block <= (a.cols - 1) / 64; block += gridDim.x) {
+        grad_columns<T, NT>(a, block);
+        __syncthreads();   // its sums are read before the next block's are written
+    }
 }
 
 // Partial rows summed: 16 columns per workgroup, four to a thread, of which 64
@@ -541,7 +544,9 @@ template <class T, class TW> int launch_back(BackArgs a, hipStream_t stream) {
         // Workgroups that read dy for the weight's gradient do not go with
         // others that write dx there: they come first then, with the same sums.
         if (!partial && (!in_registers || a.dx == a.dy)) {
-            const dim3 grid((unsigned)((a.cols + 63) / 64));
+            // As for the rows, at most 2^20 workgroups.
+            const int blocks64 = (a.cols - 1) / 64 + 1;
+            const dim3 grid((unsigned)(blocks64 < (1 << 20) ? blocks64 : 1 << 20));
             if (a.cols > 8192)
                 hipLaunchKernelGGL((weight_grad<T, 1024>), grid, dim3(1024), 0, stream, a);
             else
