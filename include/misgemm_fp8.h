@@ -69,7 +69,8 @@ extern "C" {
  *   qt, ldqt, scale_t, lds_t   x^T, cols x rows, quantised as such: its row
  *                        blocks are 128 rows of x long. Or qt NULL.
  * One pass over x makes both. One of q and qt must be given
- * (MISGEMM_NULL_OUTPUT). rows == 0 or cols == 0: nothing is done.
+ * (MISGEMM_NULL_OUTPUT). rows == 0 or cols == 0: nothing is done. More than
+ * 65,535 * 128 rows, or 2^31 - 128 columns: MISGEMM_TOO_LARGE.
  */
 int mi_fp8_quantize(int xtype, int rows, int cols, const void *x, int ldx, int ftype, int block,
                     void *q, int ldq, float *scale, int lds,
@@ -92,6 +93,8 @@ int mi_fp8_quantize(int xtype, int rows, int cols, const void *x, int ldx, int f
  * fixed for a shape, so repeated calls give identical bits.
  * beta == 0: C is not read. alpha == 0 or K == 0: A, B and their tables are
  * not read. M == 0 or N == 0: nothing is done. C must not overlap A or B.
+ * From 2^23 blocks of 128 x 128 outputs on, and where M, N or K passes
+ * 2^31 - 257: MISGEMM_TOO_LARGE.
  *
  * A call that splits k over workgroups uses the stream's workspace as
  * mi_sgemm does (see there for allocation, graph capture and release); where
