@@ -16,7 +16,7 @@ def comment(entry):
     """The comment above an entry point, its words one space apart."""
     text = open(HEADER).read()
     text = text[:text.index(f"int {entry}(")]
-    return re.sub(r"\s+(\* )?", " ", text[text.rindex("/*"):])
+    return re.sub(r"\s+", " ", re.sub(r"\n \* ?", " ", text[text.rindex("/*"):]))
 
 
 @pytest.mark.parametrize("kw", [dict(rows=65535 * 128 + 1, ldqt=MOST), dict(cols=2**31 - 127, ldx=MOST, ldq=MOST)])
