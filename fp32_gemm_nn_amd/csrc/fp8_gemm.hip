@@ -10,13 +10,16 @@
 // has some to issue.
 //
 // That instruction aligns each eight neighbouring products to the largest of
-// them and drops what is below 2^-13 of it (measured: a product of 2^-14 of
+// them and cuts off what is below 2^-13 of it (measured: a product of 2^-14 of
 // its neighbour is lost, one in another eight is not; so in every 8-bit form).
-// It puts outputs off by 2.6e-5 of their size on normal values: a hundredth of
-// the rounding to BF16, a tenth of that to FP16, but far more than FP32's own.
-// So where C is FP32 the operands become BF16 in registers, which holds both
-// 8-bit types exactly, and four v_mfma_f32_16x16x32_bf16 make the block's sum
-// (1.9e-8 off) at half the rate.
+// Against 64 bits, and before C's rounding, sums of normal values are off by
+// 0.8e-5 (E5M2 x E5M2) to 1.4e-5 (E4M3 x E4M3) of their typical size, and by
+// 1.9e-5 to 3.6e-5 where the columns differ in size (exp of 0.8 times a normal
+// value); the rounding to BF16 is off by up to 3.9e-3, that to FP16 by 4.9e-4.
+// At worst eight products lose 7 * 2^-13 of their largest. So where C is FP32,
+// whose rounding is 6e-8, the operands become BF16 in registers, which holds
+// both 8-bit types exactly, and four v_mfma_f32_16x16x32_bf16 make the block's
+// sum at half the rate (sums 6e-8 to 9e-8 off).
 //
 // The product's first operand is B and its second A: a lane then holds
 // outputs of one row of A (one sA) at neighbouring columns. Which 32 values of
