@@ -94,8 +94,11 @@ int mi_fp8_quantize(int xtype, int rows, int cols, const void *x, int ldx, int f
  * rounding. It is not bounded by C's rounding: each eight products may lose
  * 7 * 2^-13 (8.5e-4) of the largest of them, which counts where small values
  * stand beside a few large ones or large products cancel. A caller that needs
- * such sums takes C in MI_F32, and rounds it. The order of the sum is
- * fixed for a shape, so repeated calls give identical bits.
+ * such sums takes C in MI_F32, and rounds it.
+ * The order of the sum is fixed by M, N, K, C's width, `block`, whether A and B
+ * are 16-byte aligned with rows a multiple of 16 bytes apart, leading
+ * dimensions from 2^24 on, and, where k is split, whether the stream has a
+ * workspace: calls alike in these give identical bits.
  * beta == 0: C is not read. alpha == 0 or K == 0: A, B and their tables are
  * not read. M == 0 or N == 0: nothing is done. C must not overlap A or B.
  * From 2^23 blocks of 128 x 128 outputs on, and where M, N or K passes
@@ -151,7 +154,8 @@ int mi_rmsnorm(int type, int wtype, int rows, int cols, const void *x, int ldx,
  * over many rows is split over workgroups whose partial sums go through the
  * stream's workspace (as in mi_sgemm) and are added in a fixed order; for few
  * rows, and where there is no workspace, one workgroup sums all rows of its
- * columns, in the same launch.
+ * columns, in the same launch. So dweight's bits are the same for calls alike
+ * in rows, cols and whether the stream has a workspace; dx's for the same cols.
  */
 int mi_rmsnorm_backward(int type, int wtype, int rows, int cols, const void *dy, int lddy,
                         const void *h, int ldh, const void *weight, const float *rstd,
