@@ -226,6 +226,7 @@ def fp8_gemm(alpha: float, A, scale_a, B, scale_b, beta: float, C, block: str = 
 
     scale_a has a scale for each row and 128 of k; scale_b is a table of kind ``block``. C is M x N in
     float32, bfloat16 or float16; blocks are scaled and added in FP32. beta == 0: C is not read.
+    A block's two scales are multiplied first: their product has to lie between 2^-126 and 2^128.
     """
     rc = (_native or _load_native()).gemm(alpha, A, scale_a, B, scale_b, beta, C, block, stream)
     if rc is not None:

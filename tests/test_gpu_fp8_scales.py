@@ -172,3 +172,28 @@ def test_shared_k_captured_with_and_without_a_workspace(M, N, K, pad, out, block
             torch.cuda.synchronize()
             assert torch.equal(c.double(), want), (warm, rep)
         del graph
+
+
+@pytest.mark.parametrize("block", ["row", "tile"])
+@pytest.mark.parametrize("M,N,K", [(5, 9, 8), (1, 700, 2048), (64, 1024, 2048), (512, 2048, 2048), (1000, 1300, 700),
+                                   (2048, 4096, 1024), (4096, 4096, 700)])
+def test_scales_whose_product_is_at_the_edge(M, N, K, block):
+    """The least and the largest products of two scales that FP32 holds, shared out between them in different ways."""
+    g = gen(M)
+    for total, many in ((-126, 60), (127, 1)):
+        a = signs(g, M, K, E4M3)
+        b = signs(g, N, K, E5M2, min(1.0, many / K)) if many > 1 else torch.zeros(N, K, device="cuda").to(E5M2)
+        if many == 1:
+            at = torch.randint(0, K, (N,), generator=g, device="cuda")
+            b = b.float().scatter_(1, at[:, None], -1.0).to(E5M2)
+        a, b = (rows_apart(t, K + -K % 16) for t in (a, b))
+        for ea in (-110, -63, -16) if total < 0 else (110, 63, 16):
+            sa = torch.full((blocks(K), M), 2.0**ea, device="cuda")
+            sb = torch.full((blocks(K), N) if block == "row" else (blocks(N), blocks(K)), 2.0 ** (total - ea), device="cuda")
+            want = a.double() @ b.double().T.contiguous()
+            assert want.abs().max() <= (1 if many == 1 else 256)
+            for out in (torch.float32, torch.bfloat16):
+                c = torch.full((M, N), float("nan"), dtype=out, device="cuda")
+                mg.fp8_gemm(1.0, a, sa, b, sb, 0.0, c, block=block)
+                torch.cuda.synchronize()
+                assert torch.equal(c.double(), want * 2.0**total), (total, ea, out)
