@@ -97,10 +97,11 @@ int mi_fp8_quantize(int xtype, int rows, int cols, const void *x, int ldx, int f
  * such sums takes C in MI_F32, and rounds it.
  * sA(i,b) * sB(j,b) is formed first, in FP32, and so has to lie between 2^-126
  * and 2^128. Below that what a block adds loses bits (it is less than 2^-87
- * then, since a block's sum is less than 2^39), beyond it C is infinite or NaN. Scales that
- * mi_fp8_quantize makes have such products where the product of the two
- * blocks' maxima is above 2^-126 * T * T: 2.5e-33 for two E4M3 operands, 4e-29
- * for two in E5M2. Smaller operands are scaled up before they are quantised.
+ * then, since a block's sum is less than 2^39), beyond it C is infinite or
+ * NaN. Scales that mi_fp8_quantize makes have such products where the product
+ * of the two blocks' maxima is above 2^-126 * T * T: 2.5e-33 for two E4M3
+ * operands, 4e-29 for two in E5M2. Smaller operands are scaled up before they
+ * are quantised.
  * The order of the sum is fixed by M, N, K, C's width, `block`, whether A and B
  * are 16-byte aligned with rows a multiple of 16 bytes apart, leading
  * dimensions from 2^24 on, and, where k is split, whether the stream has a
