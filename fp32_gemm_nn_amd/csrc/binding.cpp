@@ -141,6 +141,13 @@ struct OnDevice {
     }
 };
 
+// For autograd: an output's values are new (an inference tensor has no version).
+void written(PyObject *o) {
+    if (!given(o)) return;
+    const at::Tensor &t = THPVariable_Unpack(o);
+    if (!t.is_inference()) t.unsafeGetTensorImpl()->bump_version();
+}
+
 // Runs `f`, which fills a status and says whether it made the call.
 template <class F> PyObject *taken(F f) {
     int status = 0;
@@ -176,6 +183,7 @@ PyObject *gemm(PyObject *, PyObject *const *a, Py_ssize_t n) {
                            reinterpret_cast<const float *>(sa.ptr), sa.ld, B.ptr, B.ld,
                            reinterpret_cast<const float *>(sb.ptr), sb.ld, beta, C.ptr, C.ld, stream);
         Py_END_ALLOW_THREADS
+        written(a[6]);
         return true;
     });
 }
@@ -209,6 +217,7 @@ PyObject *quantize(PyObject *, PyObject *const *a, Py_ssize_t n) {
                                reinterpret_cast<float *>(s.ptr), s.ld, qt.ptr, qt.ld,
                                reinterpret_cast<float *>(st.ptr), st.ld, stream);
         Py_END_ALLOW_THREADS
+        for (int i : {1, 2, 3, 4}) written(a[i]);
         return true;
     });
 }
@@ -249,6 +258,7 @@ PyObject *rmsnorm(PyObject *, PyObject *const *a, Py_ssize_t n) {
                            reinterpret_cast<float *>(out[3].ptr), out[3].ld, reinterpret_cast<float *>(out[4].ptr),
                            stream);
         Py_END_ALLOW_THREADS
+        for (int i : {4, 5, 6, 7, 8}) written(a[i]);
         return true;
     });
 }
@@ -278,6 +288,7 @@ PyObject *rmsnorm_backward(PyObject *, PyObject *const *a, Py_ssize_t n) {
                                reinterpret_cast<const float *>(rstd.ptr), dh.ptr, dh.ld, dx.ptr, dx.ld, beta,
                                reinterpret_cast<float *>(dw.ptr), stream);
         Py_END_ALLOW_THREADS
+        for (int i : {4, 5}) written(a[i]);
         return true;
     });
 }

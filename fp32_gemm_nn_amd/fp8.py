@@ -6,6 +6,9 @@ check shapes, types, devices and overlap, enqueue on ``stream`` (default: the
 current torch stream of the tensors' device, which is current for the call:
 stream 0 is its default stream) and raise on an error. Outputs
 are tensors of the caller's, written in place; nothing is computed here.
+Autograd records none of these calls: use them in a torch.autograd.Function or
+with gradients of your own. Outputs' version counters move, as with torch's
+in-place operators, so that a backward pass that saved one of them raises.
 What is plainly right goes through a C++ binding in about a microsecond; the
 checks below name what is not, and decide the rest (memory that interleaves).
 
@@ -177,6 +180,13 @@ def _raise(rc, where):
         raise MisgemmError(rc, where)
 
 
+def _written(*outs):
+    """For autograd: these tensors' values are new (an inference tensor has no version)."""
+    for t in outs:
+        if t is not None and not t.is_inference():
+            torch.autograd.graph.increment_version(t)
+
+
 def fp8_empty(rows: int, cols: int, block: str = "row", dtype=torch.float8_e4m3fn, device="cuda"):
     """An uninitialised 8-bit matrix (q, scale), its rows a multiple of 16 bytes apart."""
     q = torch.empty(rows, cols + -cols % 16, dtype=dtype, device=device)[:, :cols]
@@ -218,6 +228,7 @@ def fp8_quantize(x, q=None, scale=None, qt=None, scale_t=None, block: str = "row
     _apart(outs, ins)
     _raise(_enqueue(mi_fp8_quantize, dev, stream, _REAL[x.dtype], rows, cols, a.ptr, max(a.ld, cols),
                     _F8[given[0].dtype], _BLOCK[block], *args), "mi_fp8_quantize")
+    _written(*given)
     return tuple(given)
 
 
@@ -243,6 +254,7 @@ def fp8_gemm(alpha: float, A, scale_a, B, scale_b, beta: float, C, block: str = 
     _apart([("C", c, C.element_size())], [("A", a, 1), ("scale_a", sa, 4), ("B", b, 1), ("scale_b", sb, 4)])
     _raise(_enqueue(mi_fp8_gemm, dev, stream, _F8[A.dtype], _F8[B.dtype], _BLOCK[block], _REAL[C.dtype], M, N, K, alpha,
                     a.ptr, a.ld, sa.ptr, sa.ld, b.ptr, b.ld, sb.ptr, sb.ld, beta, c.ptr, c.ld), "mi_fp8_gemm")
+    _written(C)
     return C
 
 
@@ -292,6 +304,7 @@ def rmsnorm(x, weight, eps: float, residual=None, h=None, y=None, q=None, scale=
     _raise(_enqueue(mi_rmsnorm, dev, stream, _REAL[x.dtype], _REAL[weight.dtype], rows, cols, ax.ptr, max(ax.ld, cols),
                     ptr["residual"], ld["residual"], aw.ptr, eps, ptr["h"], ld["h"], ptr["y"], ld["y"], *qa,
                     0 if rstd is None else rstd.data_ptr()), "mi_rmsnorm")
+    _written(h, y, q, scale, rstd)
 
 
 def rmsnorm_backward(dy, h, weight, rstd, dx, dweight=None, dh=None, beta: float = 0.0, stream=None):
@@ -326,3 +339,4 @@ def rmsnorm_backward(dy, h, weight, rstd, dx, dweight=None, dh=None, beta: float
                     max(ady.ld, cols), ah.ptr, max(ah.ld, cols), aw.ptr, ar.ptr, 0 if adh is None else adh.ptr,
                     0 if adh is None else adh.ld, adx.ptr, max(adx.ld, cols), beta,
                     0 if dweight is None else dweight.data_ptr()), "mi_rmsnorm_backward")
+    _written(dx, dweight)
