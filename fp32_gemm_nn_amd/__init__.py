@@ -214,6 +214,8 @@ def sgemm(transA: str, transB: str, alpha: float, A, B, beta: float, C, stream=N
             raise TypeError(f"{name} must be float32")
         if t.device.type != "cuda":
             raise ValueError(f"{name} must be a device tensor")
+        if t.is_neg():
+            raise ValueError(f"{name} stands for the negative of its memory: pass {name}.resolve_neg()")
     if not (A.device == B.device == C.device):
         raise ValueError(f"A, B and C must be on one device (got {A.device}, {B.device}, {C.device})")
     lda, ldb, ldc = _ld(A), _ld(B), _ld(C)

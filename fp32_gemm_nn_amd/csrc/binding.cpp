@@ -60,7 +60,7 @@ bool given(PyObject *o) { return o != Py_None; }
 bool read(PyObject *o, int dims, Matrix &m) {
     if (!THPVariable_Check(o)) return false;
     const at::Tensor &t = THPVariable_Unpack(o);
-    if (!t.is_cuda() || t.layout() != at::kStrided || t.dim() != dims) return false;
+    if (!t.is_cuda() || t.layout() != at::kStrided || t.dim() != dims || t.is_neg()) return false;
     const int64_t rows = dims == 2 ? t.size(0) : 1, cols = t.size(dims - 1);
     if (rows > kMost || cols > kMost) return false;
     if (cols > 1 && t.stride(dims - 1) != 1) return false;

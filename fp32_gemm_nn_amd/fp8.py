@@ -104,6 +104,8 @@ class _Arg:
             raise ValueError(f"{name} must be on {device}, not {t.device}")
         if t.shape != shape:
             raise ValueError(f"{name} must be {tuple(shape)}, not {tuple(t.shape)}")
+        if t.is_neg():
+            raise ValueError(f"{name} stands for the negative of its memory: pass {name}.resolve_neg()")
         size = t.element_size()
         if len(shape) == 1:
             n = shape[0]
