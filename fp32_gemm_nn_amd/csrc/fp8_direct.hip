@@ -44,6 +44,7 @@ __global__ __launch_bounds__(64 * W) void fp8_direct(GemmArgs g) {
     constexpr int BM = 16 * MB, BN = 16 * NB, FRAGS = MB * NB;
     constexpr int SB = ROWB ? 4 * NB : 1;
     constexpr int LOADS = 2 * (MB + NB);   // eight rows each: A's, then B's
+    static_assert(D == 1 || D == 2, "a wave that has fewer blocks takes them one at a time");
     static_assert(kBlock % BN == 0, "a tile's columns share a block");
     static_assert(LOADS >= FRAGS, "a wave's sums fit its LDS");
     // A wave's rows of one block of k: chunk c of row r at position c ^ (r & 7),
@@ -166,10 +167,8 @@ __global__ __launch_bounds__(64 * W) void fp8_direct(GemmArgs g) {
         for (int d = 0; d < DD - 1; ++d)
             if (t + d < n) step(d, t, false);
     };
-    if (D >= 4 && n >= 4)
-        run(std::integral_constant<int, D < 4 ? D : 4>{});
-    else if (D >= 2 && n >= 2)
-        run(std::integral_constant<int, D < 2 ? D : 2>{});
+    if (D >= 2 && n >= 2)
+        run(std::integral_constant<int, D>{});
     else if (n >= 1)
         run(std::integral_constant<int, 1>{});
 

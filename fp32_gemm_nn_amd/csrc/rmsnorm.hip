@@ -223,18 +223,13 @@ struct BackArgs {
     float beta;
 };
 
-// dx of eight columns of one row, and their share of the weight's gradient.
+// dx of the `n` columns (eight at most) of one row from `col` on.
 template <class T>
 __device__ __forceinline__ void back_out(const BackArgs &a, long long row, int col, int n, const float (&dy)[8],
-                                         const float (&u)[8], const float (&w)[8], float rstd, float mean,
-                                         float (&dw)[8]) {
+                                         const float (&u)[8], const float (&w)[8], float rstd, float mean) {
     float dx[8];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-        dx[j] = rstd * (dy[j] * w[j] - u[j] * mean);
-        dw[j] = fmaf(dy[j], u[j], dw[j]);
-    }
-    if (n <= 0) return;
+    for (int j = 0; j < 8; ++j) dx[j] = rstd * (dy[j] * w[j] - u[j] * mean);
     if (a.dh != nullptr) {
         float r[8];
         load8(static_cast<const T *>(a.dh) + row * a.lddh + col, n, r);
@@ -442,13 +437,13 @@ __global__ __launch_bounds__(64 * kMaxWaves) void rmsnorm_back_long(BackArgs a) 
         const float mean = row_sum<NT>(sum, parts[turn]) / a.cols;
         for (long long c = threadIdx.x * 8; c < a.cols; c += NT * 8) {
             const int col = (int)c, n = a.cols - col;
-            float dy[8], u[8], w[8], dw[8] = {};
+            float dy[8], u[8], w[8];
             load8(static_cast<const T *>(a.dy) + row * a.lddy + col, n, dy);
             load8(static_cast<const T *>(a.h) + row * a.ldh + col, n, u);
             load8(static_cast<const TW *>(a.weight) + col, n, w);
 #pragma unroll
             for (int j = 0; j < 8; ++j) u[j] *= rstd;
-            back_out<T>(a, row, col, n, dy, u, w, rstd, mean, dw);
+            back_out<T>(a, row, col, n, dy, u, w, rstd, mean);
         }
     }
 }
