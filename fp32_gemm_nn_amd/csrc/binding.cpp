@@ -1,12 +1,13 @@
 // The tensor forms of the 8-bit linear layer, without the interpreter's time.
 //
-// A call on tensors of a layer's size costs the GPU 3 to 6 us; reading shapes,
-// strides and pointers of five tensors in Python and marshalling twenty
-// arguments through ctypes took 13 us. Here they are read through torch's C++
-// interface (about 1 us). Each function takes the Python form's arguments in
-// order, and calls the C ABI where everything about them is plainly right: it
-// returns the status. Otherwise it returns None and does nothing: fp8.py then
-// checks argument by argument, and raises the error or makes the call itself.
+// A call for one token costs the GPU 3 to 6 us; with shapes, strides and
+// pointers of five tensors read in Python and twenty arguments marshalled
+// through ctypes it took the host 13 us. Read here through torch's C++ interface
+// they take 0.4 us, and a call 3.4 to 3.9 us with its launch. Each function
+// takes the Python form's arguments in order, and calls the C ABI where
+// everything about them is plainly right: it returns the status. Otherwise it
+// returns None and does nothing: fp8.py then checks argument by argument, and
+// raises the error or makes the call itself.
 #include <Python.h>
 
 #include <torch/csrc/autograd/python_variable.h>

@@ -9,9 +9,10 @@
 // turns them into the matrix cores' operands (lane i of 16 holds row i) through
 // LDS of its own, which needs no barrier. (Loads straight into operands have
 // neighbouring lanes in different rows, and brought 13 bytes per clock and CU
-// where these bring up to 38.) 1 x 4096 x 4096 takes 5.6 us, 8192 x 8192 with
-// one row 12 us (5.6 TB/s); 64 x 4096 x 4096 6.8 us, 512 x 2048 x 2048 8.5 us,
-// where 128 x 128 tiles through LDS take 17.5, 26, 18 and 15 us.
+// where these bring up to 38.) 1 x 4096 x 4096 takes 5.3 us, 8192 x 8192 with
+// one row 11.5 us (5.8 TB/s); 64 x 4096 x 4096 6.4 us, 512 x 2048 x 2048 8.2 us,
+// where 128 x 128 tiles through LDS take 16.7, 24, 17.7 and 14.1 us (calls one
+// after another; in a graph each is 0.1 to 0.6 us longer).
 
 #include <type_traits>
 

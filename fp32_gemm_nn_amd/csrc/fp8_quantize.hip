@@ -5,8 +5,9 @@
 // scale = a / T and q = rn(x * (T / a)).
 //
 // Bound by memory: each value is read once (2 or 4 bytes) and written once or
-// twice (1 byte each). 8192 x 4096 in BF16, both ways: 25 us (5.4 TB/s, what a
-// large copy reaches); 4096 x 4096 in FP32 with tile blocks: 16.5 us (6.1 TB/s).
+// twice (1 byte each). 8192 x 4096 in BF16, both ways: 28 us (4.8 TB/s; a large
+// copy reaches 5.4); 4096 x 4096 in FP32 with tile blocks, both ways: 19.6 us
+// (5.1 TB/s).
 
 #include "fp8_common.h"
 

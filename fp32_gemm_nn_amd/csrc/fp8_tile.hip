@@ -10,17 +10,19 @@
 //
 // 256 x 256 tiles on eight waves (128 x 64 each, 128 registers of sums) halve
 // what 128 x 128 tiles read from L2 and LDS: 8192 x 8192 x 4096 to BF16 takes
-// 241 us (2.28 PFLOP/s) in the former and 294 us in the latter, two workgroups
-// of which share a CU. Below 256 tiles of 256 x 256 CUs stay empty, and the
-// smaller ones win (2048 x 4096 x 1024: 14.9 us and 20.6 us); 64 x 128 tiles
-// fill the gap to fp8_direct.hip (331 x 5752 x 352 with row scales: 7.1 us,
-// 7.7 in tiles of 128 x 128, 10.5 there). What bounds it:
-// the matrix cores are busy 57% of the time; the operands' way from L2 to LDS
-// alone takes 220 us (measured with the products left out), the products alone
-// 217 us. FP32 results (BF16 products, half the rate) are nearer to the matrix
-// cores: 4096 x 4096 x 8192 takes 241 us (1.14 PFLOP/s) with a scale for each
-// block of B and 262 us with one for each row, whose product with A's differs
-// at every output.
+// 244 us (2.25 PFLOP/s) in the former and 292 us in the latter, two workgroups
+// of which share a CU; with a scale for each row of B, whose product with A's
+// differs at every output, 286 and 324 us. Below 256 tiles of 256 x 256 CUs
+// stay empty, and the smaller ones win (2048 x 4096 x 1024: 14.5 us and 19.7
+// us); 64 x 128 tiles fill the gap to fp8_direct.hip (331 x 5752 x 352 with row
+// scales: 6.7 us, 7.3 in tiles of 128 x 128, 10.2 there). Both sides of these
+// are calls one after another on one card; cards and runs differ by 6%. What
+// bounds the large one: the matrix cores are busy 52 to 57% of the time; the
+// operands' way from L2 to LDS alone took 220 us (measured with the products
+// left out), the products alone 217 us, where the whole took 241. FP32 results
+// (BF16 products, half the rate) are nearer to the matrix cores: 4096 x 4096 x
+// 8192 takes 248 us (1.11 PFLOP/s) with a scale for each block of B and 267 us
+// with one for each row.
 
 #include "fp8_gemm.h"
 

@@ -3,11 +3,12 @@
 //
 // Both are bound by memory: every operand is read once and every output
 // written once; a row stays in registers between its sum and its use. 8192 x
-// 4096 in BF16: the norm with residual, h, y and 8 bits takes 59 us (5.1 TB/s),
-// the gradients 50 us (5.4 TB/s) and 5 us for the sum of the partial ones; a
-// copy of 256 MiB reaches 5.4 TB/s here. One row of 4096 takes 3.6 us, of
-// which a launch is 2 to 3; 333 x 1300 in FP32 with the weight's gradient in
-// the same launch 5.2 us.
+// 4096 in BF16: the norm with residual, h, y and 8 bits takes 60 us (5.0 TB/s),
+// the gradients 54 us, of which 5 are the second launch for the sum of the
+// partial ones (5.0 TB/s; 5.5 without it); a copy of 256 MiB reaches 5.4 TB/s
+// here. One row of 4096 takes 3.1 us in a graph, of which a launch is 2 to 3,
+// and 3.7 to 4.6 as a call, which is the host's time; 333 x 1300 in FP32 with
+// the weight's gradient in the same launch 5.6 us.
 
 #include "fp8_common.h"
 #include "workspace.h"
@@ -505,7 +506,7 @@ inline int back_rows(int cols) { return cols > 8192 ? 1 : 512 / back_threads(col
 // own, in the same launch, rather than from partial sums in a second one. The
 // first costs 4.5 ns a row (its workgroups take all rows one after another),
 // the second 2.6 us and the partial sums' way to memory and back at 2.4 TB/s:
-// 600 x 4096 in BF16 take 9.1 and 13.9 us, 2000 x 512 take 13.0 and 6.9 us.
+// 600 x 4096 in BF16 take 9.1 and 13.9 us, 2000 x 512 take 13.0 and 7.0 us.
 inline bool few_rows(const BackArgs &a) {
     const long long sets = ((long long)a.rows + back_rows(a.cols) - 1) / back_rows(a.cols);
     const long long groups = sets < kGroups ? sets : kGroups;

@@ -4,13 +4,14 @@ Functions with the C names (``include/misgemm_fp8.h``) take raw device
 pointers (ints) and return the C status code. The tensor forms beside them
 check shapes, types, devices and overlap, enqueue on ``stream`` (default: the
 current torch stream of the tensors' device, which is current for the call:
-stream 0 is its default stream) and raise on an error. Outputs
-are tensors of the caller's, written in place; nothing is computed here.
+stream 0 is its default stream) and raise on an error. Outputs are tensors of
+the caller's, written in place; nothing is computed here.
 Autograd records none of these calls: use them in a torch.autograd.Function or
 with gradients of your own. Outputs' version counters move, as with torch's
 in-place operators, so that a backward pass that saved one of them raises.
-What is plainly right goes through a C++ binding in about a microsecond; the
-checks below name what is not, and decide the rest (memory that interleaves).
+What is plainly right goes through a C++ binding, which reads the arguments in
+0.4 us (a call takes the host 3.4 to 3.9 us with its launch); the checks below
+name what is not, and decide the rest (memory that interleaves).
 
 An 8-bit matrix is a pair (q, scale): q of torch.float8_e4m3fn or
 torch.float8_e5m2 with contiguous rows, and a float32 table with a scale for
