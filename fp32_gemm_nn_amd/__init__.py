@@ -144,6 +144,38 @@ def mi_clock_probe(iters, stamps, stream=0):
     return rc, khz.value
 
 
+def mi_fp8_quantize(xtype, rows, cols, x, ldx, ftype, block, q, ldq, scale, lds, qt, ldqt, scale_t, lds_t,
+                    stream=0) -> int:
+    """C ABI mi_fp8_quantize with integer device pointers; returns the status code."""
+    return load_library().mi_fp8_quantize(xtype, rows, cols, x or None, ldx, ftype, block, q or None, ldq,
+                                          scale or None, lds, qt or None, ldqt, scale_t or None, lds_t,
+                                          stream or None)
+
+
+def mi_fp8_gemm(atype, btype, block, ctype, M, N, K, alpha, A, lda, scaleA, ldsa, B, ldb, scaleB, ldsb, beta, C, ldc,
+                stream=0) -> int:
+    """C ABI mi_fp8_gemm with integer device pointers; returns the status code."""
+    return load_library().mi_fp8_gemm(atype, btype, block, ctype, M, N, K, alpha, A or None, lda, scaleA or None,
+                                      ldsa, B or None, ldb, scaleB or None, ldsb, beta, C or None, ldc,
+                                      stream or None)
+
+
+def mi_rmsnorm(type, wtype, rows, cols, x, ldx, residual, ldr, weight, eps, h, ldh, y, ldy, ftype, q, ldq, scale, lds,
+               rstd, stream=0) -> int:
+    """C ABI mi_rmsnorm with integer device pointers; returns the status code."""
+    return load_library().mi_rmsnorm(type, wtype, rows, cols, x or None, ldx, residual or None, ldr, weight or None,
+                                     eps, h or None, ldh, y or None, ldy, ftype, q or None, ldq, scale or None, lds,
+                                     rstd or None, stream or None)
+
+
+def mi_rmsnorm_backward(type, wtype, rows, cols, dy, lddy, h, ldh, weight, rstd, dh, lddh, dx, lddx, beta, dweight,
+                        stream=0) -> int:
+    """C ABI mi_rmsnorm_backward with integer device pointers; returns the status code."""
+    return load_library().mi_rmsnorm_backward(type, wtype, rows, cols, dy or None, lddy, h or None, ldh,
+                                              weight or None, rstd or None, dh or None, lddh, dx or None, lddx, beta,
+                                              dweight or None, stream or None)
+
+
 def config_names() -> list[str]:
     return [mi_sgemm_config_name(i) for i in range(mi_sgemm_config_count())]
 
@@ -242,5 +274,22 @@ def sgemm(transA: str, transB: str, alpha: float, A, B, beta: float, C, stream=N
     return C
 
 
-from .fp8 import (fp8_empty, fp8_gemm, fp8_quantize, mi_fp8_gemm, mi_fp8_quantize,  # noqa: E402
-                  mi_rmsnorm, mi_rmsnorm_backward, rmsnorm, rmsnorm_backward)
+# The 8-bit layer's tensor forms need torch's types as soon as their module is
+# loaded: it is when one of them is first used, so that the package is imported
+# at once, and built where there is no torch.
+_FP8 = ("fp8_gemm", "fp8_quantize", "fp8_empty", "rmsnorm", "rmsnorm_backward")
+
+
+def __getattr__(name):
+    if name == "fp8" or name in _FP8:
+        import importlib
+
+        fp8 = importlib.import_module(".fp8", __name__)
+        for n in _FP8:
+            globals()[n] = getattr(fp8, n)
+        return globals()[name]
+    raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
+
+
+def __dir__():
+    return sorted({*globals(), "fp8", *_FP8})

@@ -61,10 +61,19 @@ def build(verbose: bool = False, extra: list[str] | None = None) -> str:
             print(" ".join(cmd), flush=True)
         procs.append((cmd, subprocess.Popen(cmd)))
         objs.append(obj)
-    cmd = binding_command(BINDING + ".tmp")
-    if verbose:
-        print(" ".join(cmd), flush=True)
-    procs.append((cmd, subprocess.Popen(cmd)))
+    # The tensor forms' binding is for torch: without it the library alone is
+    # built, and a binding of an earlier one does not stay beside it.
+    try:
+        binding = binding_command(BINDING + ".tmp")
+    except ModuleNotFoundError as e:
+        if e.name != "torch":
+            raise
+        binding = None
+        print("no torch: the library alone, without the tensor forms' binding", file=sys.stderr)
+    if binding is not None:
+        if verbose:
+            print(" ".join(binding), flush=True)
+        procs.append((binding, subprocess.Popen(binding)))
     for cmd, p in procs:
         if p.wait() != 0:
             raise subprocess.CalledProcessError(p.returncode, cmd)
@@ -73,7 +82,10 @@ def build(verbose: bool = False, extra: list[str] | None = None) -> str:
         print(" ".join(link), flush=True)
     subprocess.run(link, check=True)
     os.replace(LIB + ".tmp", LIB)
-    os.replace(BINDING + ".tmp", BINDING)
+    if binding is not None:
+        os.replace(BINDING + ".tmp", BINDING)
+    elif os.path.exists(BINDING):
+        os.remove(BINDING)
     return LIB
 
 

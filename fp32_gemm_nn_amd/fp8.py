@@ -26,7 +26,7 @@ from __future__ import annotations
 
 import torch
 
-from . import MisgemmError, load_library
+from . import MisgemmError, load_library, mi_fp8_gemm, mi_fp8_quantize, mi_rmsnorm, mi_rmsnorm_backward
 
 _REAL = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
 _F8 = {torch.float8_e4m3fn: 3, torch.float8_e5m2: 4}
@@ -58,38 +58,6 @@ def _load_native():
                 getattr(torch._C, "_cuda_exchangeDevice", lambda index: None))
     _native = module
     return module
-
-
-def mi_fp8_quantize(xtype, rows, cols, x, ldx, ftype, block, q, ldq, scale, lds, qt, ldqt, scale_t, lds_t,
-                    stream=0) -> int:
-    """C ABI mi_fp8_quantize with integer device pointers; returns the status code."""
-    return load_library().mi_fp8_quantize(xtype, rows, cols, x or None, ldx, ftype, block, q or None, ldq,
-                                          scale or None, lds, qt or None, ldqt, scale_t or None, lds_t,
-                                          stream or None)
-
-
-def mi_fp8_gemm(atype, btype, block, ctype, M, N, K, alpha, A, lda, scaleA, ldsa, B, ldb, scaleB, ldsb, beta, C, ldc,
-                stream=0) -> int:
-    """C ABI mi_fp8_gemm with integer device pointers; returns the status code."""
-    return load_library().mi_fp8_gemm(atype, btype, block, ctype, M, N, K, alpha, A or None, lda, scaleA or None,
-                                      ldsa, B or None, ldb, scaleB or None, ldsb, beta, C or None, ldc,
-                                      stream or None)
-
-
-def mi_rmsnorm(type, wtype, rows, cols, x, ldx, residual, ldr, weight, eps, h, ldh, y, ldy, ftype, q, ldq, scale, lds,
-               rstd, stream=0) -> int:
-    """C ABI mi_rmsnorm with integer device pointers; returns the status code."""
-    return load_library().mi_rmsnorm(type, wtype, rows, cols, x or None, ldx, residual or None, ldr, weight or None,
-                                     eps, h or None, ldh, y or None, ldy, ftype, q or None, ldq, scale or None, lds,
-                                     rstd or None, stream or None)
-
-
-def mi_rmsnorm_backward(type, wtype, rows, cols, dy, lddy, h, ldh, weight, rstd, dh, lddh, dx, lddx, beta, dweight,
-                        stream=0) -> int:
-    """C ABI mi_rmsnorm_backward with integer device pointers; returns the status code."""
-    return load_library().mi_rmsnorm_backward(type, wtype, rows, cols, dy or None, lddy, h or None, ldh,
-                                              weight or None, rstd or None, dh or None, lddh, dx or None, lddx, beta,
-                                              dweight or None, stream or None)
 
 
 class _Arg:
