@@ -262,13 +262,15 @@ def sgemm(transA: str, transB: str, alpha: float, A, B, beta: float, C, stream=N
     bn = int(B.shape[0] if tb else B.shape[1])
     if am != M or bk != K or bn != N:
         raise ValueError(f"shape mismatch: op(A) {am}x{K}, op(B) {bk}x{bn}, C {M}x{N}")
-    # Stream 0, torch's default one, is the current device's.
-    with torch.cuda.device(C.device):
-        if stream is None:
-            stream = torch.cuda.current_stream(C.device).cuda_stream
-        args = (transA, transB, M, N, K, alpha, A.data_ptr(), lda, B.data_ptr(), ldb, beta,
-                C.data_ptr(), ldc, stream)
-        rc = mi_sgemm(*args) if config is None else mi_sgemm_with_config(config, *args)
+    if torch.cuda.current_device() != C.device.index:
+        # Stream 0, torch's default one, is the current device's.
+        with torch.cuda.device(C.device):
+            return sgemm(transA, transB, alpha, A, B, beta, C, stream, config)
+    if stream is None:
+        stream = torch.cuda.current_stream(C.device).cuda_stream
+    args = (transA, transB, M, N, K, alpha, A.data_ptr(), lda, B.data_ptr(), ldb, beta,
+            C.data_ptr(), ldc, stream)
+    rc = mi_sgemm(*args) if config is None else mi_sgemm_with_config(config, *args)
     if rc != 0:
         raise MisgemmError(rc)
     return C

@@ -70,6 +70,7 @@ def machine(monkeypatch):
     monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda index: 0x100 * index)
     monkeypatch.setattr(torch._C, "_cuda_exchangeDevice", m.exchange)
     monkeypatch.setattr(torch.cuda, "device", m.device)
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: m.current)
     monkeypatch.setattr(torch.cuda, "current_stream", lambda device=None: Stream(device.index))
     return m
 
