@@ -5,6 +5,7 @@ tile it is made for. Operands of -1, 0 and 1 (so that the matrix cores drop noth
 have one exact result, whatever the order: each output has some 200 products that are not zero, spread over all of k,
 of which FP16 holds the sum in quarters up to 512.
 """
+import ctypes
 import sys
 
 import pytest
@@ -140,9 +141,26 @@ def test_shared_k_gives_the_same_bits_each_time(M, N, K, pad, out, block):
         assert torch.equal(c, first)
 
 
+@pytest.fixture(scope="module")
+def streams():
+    """Two streams of their own, never destroyed: torch hands its own out again, and a graph keeps the workspace of
+    the stream that it was captured on. The first never has a workspace, since nothing but captures runs on it."""
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    torch.cuda.init()
+    create = mg.load_library().hipStreamCreate       # of the HIP runtime that the library is linked against
+    create.argtypes = [ctypes.POINTER(ctypes.c_void_p)]
+    made = []
+    for _ in range(2):
+        handle = ctypes.c_void_p()
+        assert create(ctypes.byref(handle)) == 0
+        made.append(torch.cuda.ExternalStream(handle.value))
+    return made
+
+
 @pytest.mark.parametrize("block", ["row", "tile"])
 @pytest.mark.parametrize("M,N,K,pad,out", SHARED)
-def test_shared_k_captured_with_and_without_a_workspace(M, N, K, pad, out, block):
+def test_shared_k_captured_with_and_without_a_workspace(M, N, K, pad, out, block, streams):
     """A stream that is captured before it has a workspace gets a graph that does not share k, with the same exact
     result; one that has a workspace gets one that shares it."""
     g, ld = gen(4), K + -K % 16 + pad
@@ -151,12 +169,7 @@ def test_shared_k_captured_with_and_without_a_workspace(M, N, K, pad, out, block
     want = wanted(a, sa, b, sb, block)
     assert want.abs().max() <= 128          # in halves: BF16 holds them up to that
     c = torch.empty(M, N, dtype=out, device="cuda")
-    for warm in (False, True):
-        # torch hands streams out in turn: one whose workspace can go, since no graph uses it.
-        stream = next((s for s in (torch.cuda.Stream() for _ in range(64))
-                       if mg.mi_sgemm_release_workspace(s.cuda_stream) == 0), None)
-        if stream is None:
-            pytest.skip("every stream's workspace is used by a graph")
+    for warm, stream in zip((False, True), streams):
         call = lambda: mg.fp8_gemm(1.0, a, sa, b, sb, 0.0, c, block=block, stream=stream.cuda_stream)  # noqa: E731
         torch.cuda.synchronize()
         if warm:
