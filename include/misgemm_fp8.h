@@ -124,7 +124,8 @@ int mi_fp8_gemm(int atype, int btype, int block, int ctype, int M, int N, int K,
  * mi_rmsnorm: the root-mean-square norm of each row, with a residual added first.
  *
  *   h = x + residual          rounded to `type` (h = x without a residual)
- *   rstd = 1 / sqrt(mean of h^2 over the row + eps)
+ *   rstd = 1 / sqrt(mean of h^2 over the row + eps)   in FP32: 0, and so y = 0,
+ *          where the sum of h^2 passes 2^128 (from |h| = 1.8e19 on)
  *   y = h * rstd * weight     in FP32
  *   q, scale = y in 8 bits, as mi_fp8_quantize with MI_BLOCK_ROW makes it
  *              from y in FP32

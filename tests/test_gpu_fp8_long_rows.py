@@ -42,3 +42,22 @@ def test_weight_gradient(cols):
     assert ((dx[0, used].double() - want).abs() <= limit).all()
     for at in range(0, cols, 2**27):
         assert torch.isfinite(dx[0, at:at + 2**27]).all(), at
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("cols", [5, 300, 4096, 20000])
+def test_sum_of_squares_at_its_limit(cols, dtype):
+    """Squares are summed in 32 bits: up to 2^128 rstd is right, past it it is 0, and y with it."""
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    x = torch.zeros(2, cols, dtype=dtype, device="cuda")
+    x[0, cols // 2], x[1, cols // 2] = 2.0**63, 2.0**64
+    y, rstd = torch.empty_like(x), torch.empty(2, device="cuda")
+    mg.rmsnorm(x, torch.ones(cols, device="cuda"), 1e-5, y=y, rstd=rstd)
+    torch.cuda.synchronize()
+    want = (2.0**126 / cols) ** -0.5
+    # A division, a root and a reciprocal, each a step off at most; y rounds twice more, once to its type.
+    assert abs(float(rstd[0]) - want) <= 4 * 2 * U32 * want
+    want *= 2.0**63
+    assert abs(float(y[0, cols // 2]) - want) <= want * (10 * U32 + torch.finfo(dtype).eps / 2)
+    assert float(rstd[1]) == 0 and (y[1] == 0).all()
