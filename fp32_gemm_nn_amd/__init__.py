@@ -10,7 +10,9 @@ handle and return the C status code. ``sgemm`` is the torch-tensor form: it
 derives sizes and leading dimensions from the tensors, enqueues on the current
 torch stream, and raises ``MisgemmError`` on a non-zero status. So are
 ``fp8_gemm``, ``fp8_quantize``, ``rmsnorm`` and ``rmsnorm_backward`` for the
-8-bit linear layer (``include/misgemm_fp8.h``), from the module ``fp8``.
+8-bit linear layer (``include/misgemm_fp8.h``), from the module ``fp8``, and
+``linear``, ``gated``, ``act_backward`` and ``gated_backward`` for the
+feed-forward block in 16 bits (``include/misgemm_linear.h``), from ``feedforward``.
 """
 from __future__ import annotations
 
@@ -24,6 +26,8 @@ __all__ = [
     "mi_sgemm_release_workspace", "mi_clock_probe", "sgemm", "config_names",
     "mi_fp8_gemm", "mi_fp8_quantize", "mi_rmsnorm", "mi_rmsnorm_backward",
     "fp8_gemm", "fp8_quantize", "fp8_empty", "rmsnorm", "rmsnorm_backward",
+    "mi_linear", "mi_gated", "mi_act_backward", "mi_gated_backward",
+    "linear", "gated", "act_backward", "gated_backward",
 ]
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
@@ -80,6 +84,14 @@ def load_library():
     lib.mi_rmsnorm.restype = i
     lib.mi_rmsnorm_backward.argtypes = [i, i, i, i, p, i, p, i, p, p, p, i, p, i, f, p, p]
     lib.mi_rmsnorm_backward.restype = i
+    lib.mi_linear.argtypes = [c, c, i, i, i, i, f, p, i, p, i, i, p, i, i, f, p, i, p, i, i, p, i, p, i, p]
+    lib.mi_linear.restype = i
+    lib.mi_gated.argtypes = [i, i, i, i, p, i, p, i, p, i, i, p, p, i, i, p, i, i, p, i, p, i, p, i, p, i, p]
+    lib.mi_gated.restype = i
+    lib.mi_act_backward.argtypes = [i, i, i, p, i, i, i, p, i, p, i, p, i, p, i, f, p, p]
+    lib.mi_act_backward.restype = i
+    lib.mi_gated_backward.argtypes = [i, i, i, p, i, i, i, p, i, p, i, p, i, p, i, p, i, p, i, p, i, f, p, p, p]
+    lib.mi_gated_backward.restype = i
     _lib = lib
     return lib
 
@@ -174,6 +186,38 @@ def mi_rmsnorm_backward(type, wtype, rows, cols, dy, lddy, h, ldh, weight, rstd,
     return load_library().mi_rmsnorm_backward(type, wtype, rows, cols, dy or None, lddy, h or None, ldh,
                                               weight or None, rstd or None, dh or None, lddh, dx or None, lddx, beta,
                                               dweight or None, stream or None)
+
+
+def mi_linear(transA, transB, type, M, N, K, alpha, A, lda, B, ldb, biastype, bias, act, ctype, beta, R, ldr, C, ldc, ztype,
+              z, ldz, zscale, lds, stream=0) -> int:
+    """C ABI mi_linear with integer device pointers; returns the status code."""
+    return load_library().mi_linear(_ch(transA), _ch(transB), type, M, N, K, alpha, A or None, lda, B or None, ldb,
+                                    biastype, bias or None, act, ctype, beta, R or None, ldr, C or None, ldc, ztype,
+                                    z or None, ldz, zscale or None, lds, stream or None)
+
+
+def mi_gated(type, M, N, K, A, lda, G, ldg, U, ldu, biastype, biasG, biasU, act, htype, h, ldh, ztype, g, ldg_, gscale,
+             ldsg, u, ldu_, uscale, ldsu, stream=0) -> int:
+    """C ABI mi_gated with integer device pointers; returns the status code."""
+    return load_library().mi_gated(type, M, N, K, A or None, lda, G or None, ldg, U or None, ldu, biastype,
+                                   biasG or None, biasU or None, act, htype, h or None, ldh, ztype, g or None, ldg_,
+                                   gscale or None, ldsg, u or None, ldu_, uscale or None, ldsu, stream or None)
+
+
+def mi_act_backward(type, rows, cols, dy, lddy, act, ztype, z, ldz, zscale, lds, dz, lddz, y, ldy, beta, dbias,
+                    stream=0) -> int:
+    """C ABI mi_act_backward with integer device pointers; returns the status code."""
+    return load_library().mi_act_backward(type, rows, cols, dy or None, lddy, act, ztype, z or None, ldz, zscale or None,
+                                          lds, dz or None, lddz, y or None, ldy, beta, dbias or None, stream or None)
+
+
+def mi_gated_backward(type, rows, cols, dh, lddh, act, ztype, g, ldg, gscale, ldsg, u, ldu, uscale, ldsu, dg, lddg, du,
+                      lddu, h, ldh, beta, dbiasG, dbiasU, stream=0) -> int:
+    """C ABI mi_gated_backward with integer device pointers; returns the status code."""
+    return load_library().mi_gated_backward(type, rows, cols, dh or None, lddh, act, ztype, g or None, ldg,
+                                            gscale or None, ldsg, u or None, ldu, uscale or None, ldsu, dg or None,
+                                            lddg, du or None, lddu, h or None, ldh, beta, dbiasG or None,
+                                            dbiasU or None, stream or None)
 
 
 def config_names() -> list[str]:
@@ -276,22 +320,27 @@ def sgemm(transA: str, transB: str, alpha: float, A, B, beta: float, C, stream=N
     return C
 
 
-# The 8-bit layer's tensor forms need torch's types as soon as their module is
-# loaded: it is when one of them is first used, so that the package is imported
-# at once, and built where there is no torch.
+# The tensor forms of the 8-bit layer and of the feed-forward block need torch's
+# types as soon as their module is loaded: it is when one of them is first used,
+# so that the package is imported at once, and built where there is no torch.
 _FP8 = ("fp8_gemm", "fp8_quantize", "fp8_empty", "rmsnorm", "rmsnorm_backward")
+_LINEAR = ("linear", "gated", "act_backward", "gated_backward")
 
 
 def __getattr__(name):
     if name == "fp8" or name in _FP8:
-        import importlib
+        module, names = "fp8", _FP8
+    elif name == "feedforward" or name in _LINEAR:
+        module, names = "feedforward", _LINEAR
+    else:
+        raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
+    import importlib
 
-        fp8 = importlib.import_module(".fp8", __name__)
-        for n in _FP8:
-            globals()[n] = getattr(fp8, n)
-        return globals()[name]
-    raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
+    loaded = importlib.import_module("." + module, __name__)
+    for n in names:
+        globals()[n] = getattr(loaded, n)
+    return globals()[name]
 
 
 def __dir__():
-    return sorted({*globals(), "fp8", *_FP8})
+    return sorted({*globals(), "fp8", *_FP8, "feedforward", *_LINEAR})

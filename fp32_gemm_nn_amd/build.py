@@ -16,7 +16,8 @@ PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 SRCS = [os.path.join(PKG, "csrc", name) for name in ("misgemm.hip", "ladder.hip", "scratch.hip", "clock_probe.hip",
                                                 "fp8_gemm.hip", "fp8_direct.hip", "fp8_tile.hip",
-                                                "fp8_quantize.hip", "rmsnorm.hip")]
+                                                "fp8_quantize.hip", "rmsnorm.hip", "linear.hip",
+                                                "linear_tile_bf16.hip", "linear_tile_f16.hip", "act_backward.hip")]
 OBJ_DIR = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libmisgemm.so")
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
@@ -30,7 +31,7 @@ FLAGS = [
 ]
 
 
-BINDING_SRC = os.path.join(PKG, "csrc", "binding.cpp")
+BINDING_SRCS = [os.path.join(PKG, "csrc", name) for name in ("binding.cpp", "binding_linear.cpp")]
 BINDING = os.path.join(PKG, "_binding.so")
 CXX = os.environ.get("CXX", "g++")
 
@@ -47,7 +48,7 @@ def binding_command(out: str) -> list[str]:
             "-isystem", os.path.join(home, "include"),
             "-isystem", os.path.join(home, "include", "torch", "csrc", "api", "include"),
             "-isystem", sysconfig.get_paths()["include"],
-            BINDING_SRC, "-o", out, "-L" + libs, "-ltorch_python", "-ltorch_cpu", "-lc10"]
+            *BINDING_SRCS, "-o", out, "-L" + libs, "-ltorch_python", "-ltorch_cpu", "-lc10"]
 
 
 def build(verbose: bool = False, extra: list[str] | None = None) -> str:

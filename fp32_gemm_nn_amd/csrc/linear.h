@@ -1,0 +1,166 @@
+// What the kernels of the 16-bit feed-forward block share: arguments,
+// activations, and the way from sums to outputs. The mathematics is described
+// in linear.hip.
+#ifndef MISGEMM_LINEAR_KERNELS_H
+#define MISGEMM_LINEAR_KERNELS_H
+
+#include "fp8_gemm.h"
+#include "misgemm_linear.h"
+
+namespace misgemm_linear {
+
+using namespace misgemm_fp8;
+
+constexpr int kStep = 64;   // values of k to a block: 128 bytes
+
+template <class T> struct Vec {
+    typedef T x8 __attribute__((ext_vector_type(8)));
+};
+
+struct LinArgs {
+    const void *A, *B, *U;        // U: the gated block's second weight, beside B
+    const void *bias, *bias_u, *R;
+    void *C, *z, *zu;             // z: NULL where it is not kept
+    float *zs, *zus, *ws;
+    int *counters;
+    long long lda, ldb, ldu, ldr, ldc, ldz, ldzu, lds, ldsu;
+    int M, N, K;
+    int tiles_m, tiles_n, splits, kb_per_split;
+    float alpha, beta;
+    int act, ztype;
+    bool bias32, c32;             // FP32 rather than the operands' type
+    bool direct;                  // whole aligned 16 bytes everywhere: copied to LDS without registers
+};
+
+// e^x for |x| <= 104 (and NaN): 2^t with t = x / ln 2 in two parts, since the
+// rounding of t alone would be off by |x| 2^-24 of the result.
+__device__ __forceinline__ float exp_of(float x) {
+    constexpr float kLog2E = 1.44269502f, kRest = 1.92596303e-8f, kLn2 = 0.693147181f;
+    const float t = x * kLog2E;
+    const float r = fmaf(x, kRest, fmaf(x, kLog2E, -t));
+    return __builtin_amdgcn_exp2f(t) * fmaf(r, kLn2, 1.0f);
+}
+// Beyond these z every activation is at its limit in FP32. NaN stays.
+__device__ __forceinline__ float above(float z) { return z < -104.0f ? -104.0f : z; }
+__device__ __forceinline__ float within(float z) { return z > 104.0f ? 104.0f : above(z); }
+
+// 1 / (1 + e^-p).
+__device__ __forceinline__ float sigmoid(float p) { return __builtin_amdgcn_rcpf(1.0f + exp_of(-within(p))); }
+// gelu_tanh is z * sigmoid(p), p = 2 sqrt(2/pi) (z + 0.044715 z^3): (1 + tanh x) / 2 without its cancellation.
+constexpr float kGelu1 = 1.59576912f, kGelu3 = 0.0713548163f;
+__device__ __forceinline__ float gelu_p(float z) { return z * fmaf(kGelu3, z * z, kGelu1); }
+// The normal distribution's integral, without the cancellation of 1 + erf.
+__device__ __forceinline__ float normal(float z) { return 0.5f * erfcf(-0.707106781f * z); }
+
+// f(z). at(-inf) = 0 and f(inf) = inf: clamped below, where z * 0 would be NaN.
+template <int ACT> __device__ __forceinline__ float act_of(float z) {
+    if constexpr (ACT == MI_ACT_RELU) return z <= 0.0f ? 0.0f : z;
+    if constexpr (ACT == MI_ACT_SILU) return above(z) * sigmoid(z);
+    if constexpr (ACT == MI_ACT_GELU) return above(z) * normal(z);
+    if constexpr (ACT == MI_ACT_GELU_TANH) return above(z) * sigmoid(gelu_p(within(z)));
+    return z;
+}
+// f(z) and f'(z).
+template <int ACT> __device__ __forceinline__ void act_both(float z, float &f, float &df) {
+    if constexpr (ACT == MI_ACT_RELU) {
+        f = act_of<ACT>(z);
+        df = z <= 0.0f ? 0.0f : z > 0.0f ? 1.0f : z;
+    } else if constexpr (ACT == MI_ACT_SILU) {
+        const float s = sigmoid(z);
+        f = above(z) * s;
+        df = s * fmaf(within(z), 1.0f - s, 1.0f);
+    } else if constexpr (ACT == MI_ACT_GELU) {
+        const float c = within(z), s = normal(z);
+        f = above(z) * s;
+        // c * c / 2 passes 104 from 14.4 on, where the density is below FP32's least number.
+        df = fmaf(c * 0.398942280f, exp_of(-(c * c > 208.0f ? 208.0f : c * c) * 0.5f), s);
+    } else if constexpr (ACT == MI_ACT_GELU_TANH) {
+        const float c = within(z), s = sigmoid(gelu_p(c));
+        f = above(z) * s;
+        df = fmaf(c * fmaf(3.0f * kGelu3, c * c, kGelu1), s * (1.0f - s), s);
+    } else {
+        f = z;
+        df = 1.0f;
+    }
+}
+// v <- f(v), the activation chosen once for all N.
+template <int N> __device__ __forceinline__ void activate(int act, float (&v)[N]) {
+    auto all = [&](auto f) {
+#pragma unroll
+        for (int j = 0; j < N; ++j) v[j] = f(v[j]);
+    };
+    switch (act) {
+        case MI_ACT_RELU: return all([](float z) { return act_of<MI_ACT_RELU>(z); });
+        case MI_ACT_SILU: return all([](float z) { return act_of<MI_ACT_SILU>(z); });
+        case MI_ACT_GELU: return all([](float z) { return act_of<MI_ACT_GELU>(z); });
+        case MI_ACT_GELU_TANH: return all([](float z) { return act_of<MI_ACT_GELU_TANH>(z); });
+        default: return;
+    }
+}
+
+// N neighbouring values of the bias, zero without one and past the row.
+template <class T, int N> __device__ __forceinline__ void bias_at(const void *bias, bool f32, int n, int left, float (&v)[N]) {
+    if (bias == nullptr) {
+#pragma unroll
+        for (int j = 0; j < N; ++j) v[j] = 0.0f;
+    } else if (f32) {
+        load<float, N>(static_cast<const float *>(bias) + n, left, v);
+    } else {
+        load<T, N>(static_cast<const T *>(bias) + n, left, v);
+    }
+}
+
+// One row's N neighbouring values from column n on: z (unless it has 8 bits),
+// then f(z) + beta R. R may be C: a value is read by the thread that writes it.
+template <class CT, int N> __device__ __forceinline__ void put_linear(const LinArgs &g, int m, int n, float (&v)[N]) {
+    const int left = g.N - n;
+    if (g.z != nullptr && g.zs == nullptr) store<CT, N>(static_cast<CT *>(g.z) + m * g.ldz + n, left, v);
+    activate<N>(g.act, v);
+    if (g.beta != 0.0f) {
+        float r[N];
+        load<CT, N>(static_cast<const CT *>(g.R) + m * g.ldr + n, left, r);
+#pragma unroll
+        for (int j = 0; j < N; ++j) v[j] = fmaf(g.beta, r[j], v[j]);
+    }
+    store<CT, N>(static_cast<CT *>(g.C) + m * g.ldc + n, left, v);
+}
+// The gated block's: v is g and then h, u is u.
+template <class CT, int N>
+__device__ __forceinline__ void put_gated(const LinArgs &g, int m, int n, float (&v)[N], const float (&u)[N]) {
+    const int left = g.N - n;
+    if (g.z != nullptr && g.zs == nullptr) {
+        store<CT, N>(static_cast<CT *>(g.z) + m * g.ldz + n, left, v);
+        store<CT, N>(static_cast<CT *>(g.zu) + m * g.ldzu + n, left, u);
+    }
+    activate<N>(g.act, v);
+#pragma unroll
+    for (int j = 0; j < N; ++j) v[j] *= u[j];
+    store<CT, N>(static_cast<CT *>(g.C) + m * g.ldc + n, left, v);
+}
+template <class T, bool GATED, int N>
+__device__ __forceinline__ void put_out(const LinArgs &g, int m, int n, float (&v)[N], const float (&u)[N]) {
+    if (m >= g.M || n >= g.N) return;
+    if constexpr (GATED) {
+        if (g.c32)
+            put_gated<float, N>(g, m, n, v, u);
+        else
+            put_gated<T, N>(g, m, n, v, u);
+    } else {
+        if (g.c32)
+            put_linear<float, N>(g, m, n, v);
+        else
+            put_linear<T, N>(g, m, n, v);
+    }
+}
+
+inline bool is_half(int t) { return t == MI_BF16 || t == MI_F16; }
+
+// Tiles that go through LDS (linear_tile.h, one file for each type), and
+// products of few rows without a barrier in their sum (linear_direct.hip).
+// `shape` names one of their tile shapes.
+int launch_tiles_bf16(bool gated, bool ta, bool tb, int shape, LinArgs &g, hipStream_t stream);
+int launch_tiles_f16(bool gated, bool ta, bool tb, int shape, LinArgs &g, hipStream_t stream);
+
+}  // namespace misgemm_linear
+
+#endif  // MISGEMM_LINEAR_KERNELS_H

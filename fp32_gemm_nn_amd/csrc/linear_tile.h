@@ -1,0 +1,476 @@
+// Products of many outputs in 16 bits, in tiles of BM x BN whose operands go
+// through LDS. One translation unit for each type includes this.
+#ifndef MISGEMM_LINEAR_TILE_H
+#define MISGEMM_LINEAR_TILE_H
+
+#include "linear.h"
+
+namespace misgemm_linear {
+namespace {
+
+// 16 bytes a lane from base + offset to LDS, 64 lanes' side by side from `lds`
+// on. In assembly, since the compiler would have every later read of LDS wait
+// for it: the reads here are of another buffer until `meet`. It writes no register.
+__device__ __forceinline__ void load_lds(const void *base, uint32_t offset, const uint8_t *lds) {
+    const uint32_t to =
+        (uint32_t)reinterpret_cast<size_t>((const __attribute__((address_space(3))) uint8_t *)lds);
+    asm volatile("s_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"{m0}"(to), "v"(offset), "s"(base) : "memory");
+}
+
+// The waves of a workgroup meet, with all they have read and written in LDS
+// done, and all they load to LDS landed.
+__device__ __forceinline__ void meet() {
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_waitcnt(0);
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+}
+
+template <class T> __device__ __forceinline__ f32x4 product(typename Vec<T>::x8 a, typename Vec<T>::x8 b, f32x4 c) {
+    if constexpr (std::is_same<T, bf16>::value)
+        return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
+    else
+        return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0);
+}
+
+// One operand's block of 64 values of k for ROWS rows of outputs, in LDS in
+// 16-byte chunks, chunk q of thread q % NT. KMAJOR: memory has k running
+// fastest; LDS holds rows of eight chunks, chunk c of row r at c ^ (r & 7).
+// Otherwise memory has the outputs' rows running fastest; LDS holds 64 rows of
+// k, whose pairs of chunks (16 values) are moved by turn(k), and the matrix
+// cores' operands come through the transposing read: lane l of 16 names four
+// values of row k = l / 4, and gets the l-th of each of four rows. Either way
+// the lanes that read at once touch all banks.
+template <class T, int ROWS, int NT, bool KMAJOR> struct Panel {
+    static constexpr int PER = ROWS * 8 / NT, CHUNKS = KMAJOR ? 8 : ROWS / 8;
+    static_assert(PER * NT == ROWS * 8 && NT % 64 == 0 && ROWS >= 64, "whole chunks per thread");
+    static __device__ __forceinline__ int turn(int k) {
+        if constexpr (ROWS >= 128) return (k & 3) | (k >> 1 & 4);
+        return (k >> 1 & 1) | (k >> 2 & 2);
+    }
+    // Of chunk q = tid + NT * j: its row in LDS, and its chunk in memory's row.
+    static __device__ __forceinline__ int row(int tid, int j) { return (tid + NT * j) / CHUNKS; }
+    static __device__ __forceinline__ int chunk(int tid, int j) {
+        const int r = row(tid, j);
+        return (tid + NT * j) % CHUNKS ^ (KMAJOR ? r & 7 : 2 * turn(r));
+    }
+    // Where this lane reads 16 rows of outputs from `first` on.
+    static __device__ __forceinline__ uint32_t at(int first, int lane) {
+        const int i = lane % 16, grp = lane / 16;
+        if constexpr (KMAJOR)
+            return (first + i) * 128 + 16 * (grp ^ (i & 7));
+        else
+            return (8 * grp + i / 4) * (2 * ROWS) + 32 * (first / 16 ^ turn(8 * grp + i / 4)) + 8 * (i % 4);
+    }
+    // The operand of k values 32 s .. 32 s + 31 of the a-th 16 rows from there,
+    // of at most eight (four where ROWS is 64), whose first is a multiple of as many.
+    static __device__ __forceinline__ typename Vec<T>::x8 read(const uint8_t *lds, uint32_t at, int a, int s) {
+        typedef short short4v __attribute__((ext_vector_type(4)));
+        typedef short short8v __attribute__((ext_vector_type(8)));
+        if constexpr (KMAJOR) {
+            return *reinterpret_cast<const typename Vec<T>::x8 *>(lds + (at ^ 64 * s) + 2048 * a);
+        } else {
+            typedef __attribute__((address_space(3))) short4v lds4;
+            lds4 *p = (lds4 *)(lds + (at ^ 32 * a) + 32 * s * (2 * ROWS));
+            const short4v lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16(p);
+            const short4v hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16(p + ROWS);   // four rows of k on
+            const short8v v = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+            return __builtin_bit_cast(typename Vec<T>::x8, v);
+        }
+    }
+};
+
+// Eight values of a row of `cols` from column col on, zeros past its end, in
+// two steps: as they are read, and once they have come. `live`: the row is one.
+template <class T> struct Chunk {
+    i32x4 w;
+    typedef int words __attribute__((ext_vector_type(4), aligned(2)));
+    __device__ __forceinline__ void fetch(const T *row, int col, int cols) {
+        if (cols >= 8) {
+            w = *reinterpret_cast<const words *>(row + min(col, cols - 8));
+        } else {
+            uint32_t v[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                v[j] = col + j < cols ? reinterpret_cast<const uint16_t *>(row)[col + j] : 0;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) w[j] = (int)(v[2 * j] | v[2 * j + 1] << 16);
+        }
+    }
+    __device__ __forceinline__ void settle(int col, int cols, bool live) {
+        if (cols >= 8) w = shifted(w, 2 * max(col - (cols - 8), 0));
+#pragma unroll
+        for (int j = 0; j < 4; ++j) w[j] = live ? w[j] : 0;
+    }
+};
+
+enum Way { DIRECT, STAGED };   // operands to LDS: without registers, or through them at any alignment
+
+template <class T, int BM, int BN, int WM, int WN, bool KA, bool KB, bool GATED, Way WAY>
+__global__ __launch_bounds__(64 * WM * WN, WM * WN == 8 ? 2 : BM * BN > 128 * 128 ? 1 : 2) void lin_tile(LinArgs g) {
+    constexpr int NT = 64 * WM * WN, TM = BM / WM, TN = BN / WN, MI = TM / 16, NI = TN / 16;
+    static_assert(!GATED || (KB && BN == 256), "a tile has 128 columns of both projections");
+    static_assert(TN == 64 || TN == 128, "");
+    using PanelA = Panel<T, BM, NT, KA>;
+    using PanelB = Panel<T, BN, NT, KB>;
+    using x8 = typename Vec<T>::x8;
+    constexpr int BYTES = (BM + BN) * 128;
+    // After the sums: 16 * ROWS rows of 64 outputs of each wave, and rows' maxima.
+    constexpr int ROWS = MI < 4 ? MI : 4, TURN = WM * WN * ROWS * 16 * 64 * 4, MAXES = 4 * BM * WN * (GATED ? 2 : 1);
+    constexpr int LDS = 2 * BYTES > TURN + MAXES ? 2 * BYTES : TURN + MAXES;
+    __shared__ __align__(1024) uint8_t lds[LDS];
+    const int tid = threadIdx.x, lane = tid % 64, wave = __builtin_amdgcn_readfirstlane(tid / 64);
+    const int i = lane % 16, grp = lane / 16;
+    const int wm = wave / WN, wn = wave % WN;
+
+    int tm, tn;
+    const int tiles = g.tiles_m * g.tiles_n;
+    const int split = blockIdx.x / tiles, tile = blockIdx.x - split * tiles;
+    tile_of(tile, g.tiles_m, g.tiles_n, tm, tn);
+    constexpr int COLS = GATED ? BN / 2 : BN;   // of outputs
+    const int m0 = tm * BM, n0 = tn * COLS;
+    const int kblocks = (g.K + kStep - 1) / kStep;
+    const int kb0 = split * g.kb_per_split, kb1 = min(kblocks, kb0 + g.kb_per_split);
+    const T *A = static_cast<const T *>(g.A), *B = static_cast<const T *>(g.B), *U = static_cast<const T *>(g.U);
+
+    // The gated tile's rows of B: each wave has TN / 2 of the first weight's and as many of the second's, of the same columns.
+    auto second = [](int r) { return GATED && r % TN >= TN / 2; };
+    auto column = [](int r) { return GATED ? r / TN * (TN / 2) + r % (TN / 2) : r; };
+
+    uint32_t from_a[PanelA::PER], from_b[PanelB::PER];
+    if constexpr (WAY == DIRECT) {
+        // Rows and chunks past the matrix repeat its last ones: their outputs are not stored.
+#pragma unroll
+        for (int j = 0; j < PanelA::PER; ++j) {
+            const int r = PanelA::row(tid, j), c = PanelA::chunk(tid, j);
+            from_a[j] = KA ? min(r, g.M - 1 - m0) * (uint32_t)g.lda * 2 + 16 * c
+                           : r * (uint32_t)g.lda * 2 + 16 * min(c, (g.M - m0) / 8 - 1);
+        }
+#pragma unroll
+        for (int j = 0; j < PanelB::PER; ++j) {
+            const int r = PanelB::row(tid, j), c = PanelB::chunk(tid, j);
+            const uint32_t ld = second(r) ? (uint32_t)g.ldu : (uint32_t)g.ldb;
+            from_b[j] = KB ? min(column(r), g.N - 1 - n0) * ld * 2 + 16 * c
+                           : r * ld * 2 + 16 * min(c, (g.N - n0) / 8 - 1);
+        }
+    }
+    auto copy_a = [&](int kb, int buf, int j) {
+        const T *src = KA ? A + m0 * g.lda + (long long)kb * kStep : A + (long long)kb * kStep * g.lda + m0;
+        load_lds(src, from_a[j], lds + buf * BYTES + 1024 * wave + 16 * NT * j);
+    };
+    auto copy_b = [&](int kb, int buf, int j) {
+        // A wave's 64 chunks are eight rows, of one weight.
+        const T *src;
+        if constexpr (KB) {
+            const bool u = second(8 * wave + NT / 8 * j);
+            src = (u ? U + n0 * g.ldu : B + n0 * g.ldb) + (long long)kb * kStep;
+        } else {
+            src = B + (long long)kb * kStep * g.ldb + n0;
+        }
+        load_lds(src, from_b[j], lds + buf * BYTES + BM * 128 + 1024 * wave + 16 * NT * j);
+    };
+    auto copy = [&](int kb, int buf) {
+#pragma unroll
+        for (int j = 0; j < PanelA::PER; ++j) copy_a(kb, buf, j);
+#pragma unroll
+        for (int j = 0; j < PanelB::PER; ++j) copy_b(kb, buf, j);
+    };
+    struct Chunks {
+        Chunk<T> a[PanelA::PER], b[PanelB::PER];
+    };
+    auto fetch = [&](Chunks &w, int kb) {
+        const int k0 = kb * kStep;
+#pragma unroll
+        for (int j = 0; j < PanelA::PER; ++j) {
+            const int r = PanelA::row(tid, j), c = 8 * PanelA::chunk(tid, j);
+            if (KA)
+                w.a[j].fetch(A + min(m0 + r, g.M - 1) * g.lda, k0 + c, g.K);
+            else
+                w.a[j].fetch(A + min(k0 + r, g.K - 1) * g.lda, m0 + c, g.M);
+        }
+#pragma unroll
+        for (int j = 0; j < PanelB::PER; ++j) {
+            const int r = PanelB::row(tid, j), c = 8 * PanelB::chunk(tid, j);
+            if (KB)
+                w.b[j].fetch((second(r) ? U : B) + min(n0 + column(r), g.N - 1) * (second(r) ? g.ldu : g.ldb), k0 + c, g.K);
+            else
+                w.b[j].fetch(B + min(k0 + r, g.K - 1) * g.ldb, n0 + c, g.N);
+        }
+    };
+    auto write = [&](Chunks &w, int kb, int buf) {
+        const int k0 = kb * kStep;
+        const bool edge = k0 + kStep > g.K;
+        if (edge || (!KA && m0 + BM > g.M)) {
+#pragma unroll
+            for (int j = 0; j < PanelA::PER; ++j) {
+                const int r = PanelA::row(tid, j), c = 8 * PanelA::chunk(tid, j);
+                w.a[j].settle((KA ? k0 : m0) + c, KA ? g.K : g.M, KA || k0 + r < g.K);
+            }
+        }
+        if (edge || (!KB && n0 + BN > g.N)) {
+#pragma unroll
+            for (int j = 0; j < PanelB::PER; ++j) {
+                const int r = PanelB::row(tid, j), c = 8 * PanelB::chunk(tid, j);
+                w.b[j].settle((KB ? k0 : n0) + c, KB ? g.K : g.N, KB || k0 + r < g.K);
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < PanelA::PER; ++j)
+            *reinterpret_cast<i32x4 *>(lds + buf * BYTES + 16 * (tid + NT * j)) = w.a[j].w;
+#pragma unroll
+        for (int j = 0; j < PanelB::PER; ++j)
+            *reinterpret_cast<i32x4 *>(lds + buf * BYTES + BM * 128 + 16 * (tid + NT * j)) = w.b[j].w;
+    };
+
+    f32x4 acc[MI][NI];
+#pragma unroll
+    for (int a = 0; a < MI; ++a)
+#pragma unroll
+        for (int b = 0; b < NI; ++b) acc[a][b] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+
+    // Operands of half a block each: one half's products run while the other's are read.
+    struct Half {
+        x8 a[MI], b[NI];
+    };
+    Half half[2];
+    const uint32_t at_a = PanelA::at(wm * TM, lane), at_b = PanelB::at(wn * TN, lane);
+    auto read = [&](int buf, int s, int p) {
+        Half &h = half[s];
+        if (p < NI)
+            h.b[p] = PanelB::read(lds + buf * BYTES + BM * 128, at_b, p, s);
+        else
+            h.a[p - NI] = PanelA::read(lds + buf * BYTES, at_a, p - NI, s);
+    };
+    constexpr int READS = MI + NI;
+    // The products of one half; before each row of them some of the next half's reads, and of `more`.
+    auto multiply = [&](int s, int next_buf, auto more) {
+#pragma unroll
+        for (int a = 0; a < MI; ++a) {
+#pragma unroll
+            for (int p = READS * a / MI; p < READS * (a + 1) / MI; ++p) read(next_buf, s ^ 1, p);
+            more(a);
+#pragma unroll
+            for (int b = 0; b < NI; ++b) acc[a][b] = product<T>(half[s].b[b], half[s].a[a], acc[a][b]);
+            __builtin_amdgcn_sched_barrier(0);
+        }
+    };
+    auto nothing = [](int) {};
+
+    const int last = WAY == STAGED ? kb1 : min(kb1, g.K / kStep);   // the blocks that the loop takes
+    if (kb0 < last) {
+        Chunks w;
+        if constexpr (WAY == STAGED) {
+            fetch(w, kb0);
+            write(w, kb0, 0);
+            if (kb0 + 1 < last) fetch(w, kb0 + 1);
+        } else {
+            copy(kb0, 0);
+        }
+        meet();
+        if constexpr (WAY == STAGED) {
+            if (kb0 + 1 < last) write(w, kb0 + 1, 1);
+        } else {
+            if (kb0 + 1 < last) copy(kb0 + 1, 1);
+        }
+#pragma unroll
+        for (int p = 0; p < READS; ++p) read(0, 0, p);
+#pragma unroll 1
+        for (int kb = kb0; kb < last; ++kb) {
+            const int buf = (kb - kb0) & 1;
+            if constexpr (WAY == STAGED) {
+                if (kb + 2 < last) fetch(w, kb + 2);
+            }
+            multiply(0, buf, nothing);
+            // All of this block is in registers, and the next one has landed.
+            meet();
+            if constexpr (WAY == STAGED) {
+                if (kb + 2 < last) write(w, kb + 2, buf);
+                multiply(1, buf ^ 1, nothing);
+            } else {
+                if (kb + 2 < last) copy(kb + 2, buf);
+                multiply(1, buf ^ 1, nothing);
+            }
+        }
+    }
+    if constexpr (WAY == DIRECT) {
+        if (last < kb1) {   // the last block of k, where it is short
+            Chunks w;
+            fetch(w, last);
+            meet();
+            write(w, last, 0);
+            meet();
+#pragma unroll
+            for (int p = 0; p < READS; ++p) read(0, 0, p);
+            multiply(0, 0, nothing);
+            multiply(1, 0, nothing);
+        }
+    }
+
+    if (g.splits > 1) {
+        // Partial tiles go to the workspace, written and read past the XCDs'
+        // own caches; the last workgroup of a tile adds them in split order.
+        constexpr int PART = BM * BN;
+        float *part = g.ws + ((size_t)tile * g.splits) * PART + (size_t)wave * (MI * NI * 4 * 64) + lane;
+#pragma unroll
+        for (int a = 0; a < MI; ++a)
+#pragma unroll
+            for (int b = 0; b < NI; ++b)
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    __hip_atomic_store(part + (size_t)split * PART + ((a * NI + b) * 4 + j) * 64, acc[a][b][j],
+                                       __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        __builtin_amdgcn_s_waitcnt(0);
+        __syncthreads();
+        int *is_last = reinterpret_cast<int *>(lds);   // of the operands' memory, which is read no more
+        if (tid == 0)
+            *is_last = __hip_atomic_fetch_add(&g.counters[tile], 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) ==
+                      g.splits - 1;
+        __syncthreads();
+        if (!*is_last) return;
+        if (tid == 0) __hip_atomic_store(&g.counters[tile], 0, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+#pragma unroll
+        for (int a = 0; a < MI; ++a)
+#pragma unroll
+            for (int b = 0; b < NI; ++b) acc[a][b] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+        for (int s = 0; s < g.splits; ++s)
+#pragma unroll
+            for (int a = 0; a < MI; ++a)
+#pragma unroll
+                for (int b = 0; b < NI; ++b)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        acc[a][b][j] += __hip_atomic_load(part + (size_t)s * PART + ((a * NI + b) * 4 + j) * 64,
+                                                          __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    }
+
+    // z: a lane holds row 16 a + i and columns 16 b + 4 grp + 0..3 of its wave's.
+    meet();
+    const int m1 = m0 + wm * TM, n1 = n0 + wn * (GATED ? TN / 2 : TN);
+    constexpr int NH = GATED ? NI / 2 : NI;   // sixteens of columns of outputs
+#pragma unroll
+    for (int b = 0; b < NI; ++b) {
+        const int n = n1 + 16 * (b % NH) + 4 * grp;
+        float bias[4];
+        bias_at<T, 4>(b < NH ? g.bias : g.bias_u, g.bias32, n, g.N - n, bias);
+#pragma unroll
+        for (int a = 0; a < MI; ++a)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) acc[a][b][j] = fmaf(g.alpha, acc[a][b][j], bias[j]);
+    }
+    // Largest |z| of each row and 128 columns, which SHARE waves have.
+    constexpr int SHARE = GATED ? WN : 128 / TN;
+    float *maxes = reinterpret_cast<float *>(lds + TURN);
+    const bool in8 = g.zs != nullptr;
+    if (in8) {
+#pragma unroll
+        for (int half = 0; half < (GATED ? 2 : 1); ++half)
+#pragma unroll
+            for (int a = 0; a < MI; ++a) {
+                float m = 0.0f;
+#pragma unroll
+                for (int b = half * NH; b < (half + 1) * NH; ++b)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        m = fmaxf(m, n1 + 16 * (b - half * NH) + 4 * grp + j < g.N ? fabsf(acc[a][b][j]) : 0.0f);
+                m = fmaxf(m, __shfl_xor(m, 16));
+                m = fmaxf(m, __shfl_xor(m, 32));
+                if (grp == 0) maxes[(half * WN + wn) * BM + wm * TM + 16 * a + i] = m;
+            }
+        __syncthreads();
+    }
+    // Outputs turn in LDS, each wave's in its own, and leave as whole rows:
+    // 64 columns at a time, or 32 and 32 of the two projections. Chunk c (four
+    // values) of row r is at c ^ (r & 15).
+    f32x4 *own = reinterpret_cast<f32x4 *>(lds) + wave * ROWS * 256;
+    constexpr int LANES = GATED ? 4 : 8;   // of a row
+#pragma unroll
+    for (int p = 0; p < NI / 4; ++p)
+#pragma unroll
+        for (int a0 = 0; a0 < MI; a0 += ROWS) {
+#pragma unroll
+            for (int a = 0; a < ROWS; ++a)
+#pragma unroll
+                for (int b = 0; b < 4; ++b)
+                    own[(16 * a + i) * 16 + ((4 * b + grp) ^ i)] =
+                        acc[a0 + a][GATED ? (b < 2 ? 2 * p + b : NH + 2 * p + b - 2) : 4 * p + b];
+            asm volatile("" ::: "memory");
+#pragma unroll 1
+            for (int r0 = 0; r0 < 16 * ROWS; r0 += 64 / LANES) {
+                const int r = r0 + lane / LANES, c = lane % LANES * 2;
+                const int m = m1 + 16 * a0 + r, n = n1 + (GATED ? 32 : 64) * p + 4 * c;
+                float v[8], u[8];
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const f32x4 x = own[r * 16 + ((c + h) ^ (r & 15))];
+                    f32x4 y = {};
+                    if constexpr (GATED) y = own[r * 16 + ((8 + c + h) ^ (r & 15))];
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        v[4 * h + j] = x[j];
+                        u[4 * h + j] = y[j];
+                    }
+                }
+                if (in8 && m < g.M && n < g.N) {
+                    auto keep = [&](const float (&z)[8], int half, uint8_t *q, long long ldq, float *table, long long lds_) {
+                        float most = kTiny;
+#pragma unroll
+                        for (int w = 0; w < SHARE; ++w)
+                            most = fmaxf(most, maxes[(half * WN + wn / SHARE * SHARE + w) * BM + wm * TM + 16 * a0 + r]);
+                        const float top_ = g.ztype == MI_E4M3 ? top<MI_E4M3>() : top<MI_E5M2>(), f = top_ / most;
+                        const int words[2] = {
+                            g.ztype == MI_E4M3 ? pack4<MI_E4M3>(z[0] * f, z[1] * f, z[2] * f, z[3] * f)
+                                               : pack4<MI_E5M2>(z[0] * f, z[1] * f, z[2] * f, z[3] * f),
+                            g.ztype == MI_E4M3 ? pack4<MI_E4M3>(z[4] * f, z[5] * f, z[6] * f, z[7] * f)
+                                               : pack4<MI_E5M2>(z[4] * f, z[5] * f, z[6] * f, z[7] * f)};
+                        store_bytes<8>(q + m * ldq + n, g.N - n, words);
+                        if (n % kBlock == 0) table[n / kBlock * lds_ + m] = most / top_;
+                    };
+                    keep(v, 0, static_cast<uint8_t *>(g.z), g.ldz, g.zs, g.lds);
+                    if constexpr (GATED) keep(u, 1, static_cast<uint8_t *>(g.zu), g.ldzu, g.zus, g.ldsu);
+                }
+                put_out<T, GATED, 8>(g, m, n, v, u);
+            }
+            asm volatile("" ::: "memory");
+        }
+}
+
+template <class T, int BM, int BN, int WM, int WN, bool KA, bool KB, bool GATED, Way WAY>
+int launch_tile(LinArgs &g, bool split, hipStream_t stream) {
+    constexpr int COLS = GATED ? BN / 2 : BN;
+    g.tiles_m = (g.M + BM - 1) / BM;
+    g.tiles_n = (g.N + COLS - 1) / COLS;
+    const int kblocks = (g.K + kStep - 1) / kStep;
+    const long long tiles = (long long)g.tiles_m * g.tiles_n;
+    g.splits = split ? splits_of(tiles, kblocks) : 1;
+    static_assert((size_t)2 * kNumCus * 64 * 256 <= misgemm_workspace::kFloats &&
+                  2 * kNumCus <= misgemm_workspace::kCounters, "partial tiles fit the workspace");
+    if (g.splits > 1 && !misgemm_workspace::get(stream, &g.ws, &g.counters)) g.splits = 1;
+    g.kb_per_split = (kblocks + g.splits - 1) / g.splits;
+    hipLaunchKernelGGL((lin_tile<T, BM, BN, WM, WN, KA, KB, GATED, WAY>), dim3((unsigned)(tiles * g.splits)),
+                       dim3(64 * WM * WN), 0, stream, g);
+    return launched();
+}
+
+template <class T, bool KA, bool KB> int launch_linear(int shape, LinArgs &g, hipStream_t stream) {
+    switch (shape) {
+        default: return launch_tile<T, 128, 128, 2, 2, KA, KB, false, STAGED>(g, true, stream);
+    }
+}
+template <class T> int launch_gated(int shape, LinArgs &g, hipStream_t stream) {
+    switch (shape) {
+        default: return launch_tile<T, 64, 256, 2, 2, true, true, true, STAGED>(g, true, stream);
+    }
+}
+
+// ta, tb: A is K x M, B is N x K in memory.
+template <class T> int launch_tiles(bool gated, bool ta, bool tb, int shape, LinArgs &g, hipStream_t stream) {
+    if (gated) return launch_gated<T>(shape, g, stream);
+    if (ta)
+        return tb ? launch_linear<T, false, true>(shape, g, stream) : launch_linear<T, false, false>(shape, g, stream);
+    return tb ? launch_linear<T, true, true>(shape, g, stream) : launch_linear<T, true, false>(shape, g, stream);
+}
+
+}  // namespace
+}  // namespace misgemm_linear
+
+#endif  // MISGEMM_LINEAR_TILE_H

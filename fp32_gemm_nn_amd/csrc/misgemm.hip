@@ -81,6 +81,7 @@
 
 #include "misgemm.h"
 #include "misgemm_fp8.h"
+#include "misgemm_linear.h"
 #include "ladder.h"
 #include "scratch.h"
 #include "skinny_kernels.h"
@@ -1108,6 +1109,7 @@ extern "C" const char *mi_sgemm_status_string(int status) {
         case MISGEMM_NULL_SCALE: return "a scale table is null";
         case MISGEMM_BAD_LD: return "a leading dimension smaller than its row";
         case MISGEMM_BAD_LDS: return "a scale table's leading dimension smaller than its row";
+        case MISGEMM_BAD_ACT: return "unknown activation";
         case MISGEMM_WORKSPACE_CAPTURED: return "workspace is used by a captured HIP graph and stays allocated until the process ends";
         default: return "unknown status";
     }
