@@ -16,7 +16,7 @@ PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 SRCS = [os.path.join(PKG, "csrc", name) for name in ("misgemm.hip", "ladder.hip", "scratch.hip", "clock_probe.hip",
                                                 "fp8_gemm.hip", "fp8_direct.hip", "fp8_tile.hip",
-                                                "fp8_quantize.hip", "rmsnorm.hip", "linear.hip",
+                                                "fp8_quantize.hip", "rmsnorm.hip", "linear.hip", "linear_direct.hip",
                                                 "linear_tile_bf16.hip", "linear_tile_f16.hip", "act_backward.hip")]
 OBJ_DIR = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libmisgemm.so")

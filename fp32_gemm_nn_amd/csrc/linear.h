@@ -32,32 +32,56 @@ struct LinArgs {
     bool direct;                  // whole aligned 16 bytes everywhere: copied to LDS without registers
 };
 
-// e^x for |x| <= 104 (and NaN): 2^t with t = x / ln 2 in two parts, since the
-// rounding of t alone would be off by |x| 2^-24 of the result.
-__device__ __forceinline__ float exp_of(float x) {
-    constexpr float kLog2E = 1.44269502f, kRest = 1.92596303e-8f, kLn2 = 0.693147181f;
-    const float t = x * kLog2E;
-    const float r = fmaf(x, kRest, fmaf(x, kLog2E, -t));
-    return __builtin_amdgcn_exp2f(t) * fmaf(r, kLn2, 1.0f);
-}
-// Beyond these z every activation is at its limit in FP32. NaN stays.
-__device__ __forceinline__ float above(float z) { return z < -104.0f ? -104.0f : z; }
-__device__ __forceinline__ float within(float z) { return z > 104.0f ? 104.0f : above(z); }
+// f in few instructions: an epilogue forms 128 of them a lane while the matrix
+// cores wait, and v_exp_f32 and v_rcp_f32 take as long as four others. Their
+// steps of a result's last place are the least error there is; e^x as 2^(x / ln 2)
+// is off by |x| of them at most. Where z is infinite a factor that would make
+// NaN of the other's 0 is held at 104, beyond which f and f' are at their limits
+// (v_max_f32 and v_min_f32 drop NaN, so the other factor has to carry it).
+constexpr float kLog2E = 1.44269504f;
+__device__ __forceinline__ float above(float z) { return fmaxf(z, -104.0f); }
+__device__ __forceinline__ float within(float z) { return fminf(fmaxf(z, -104.0f), 104.0f); }
 
-// 1 / (1 + e^-p).
-__device__ __forceinline__ float sigmoid(float p) { return __builtin_amdgcn_rcpf(1.0f + exp_of(-within(p))); }
+// 1 / (1 + e^-z).
+__device__ __forceinline__ float sigmoid(float z) {
+    return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(z * -kLog2E));
+}
 // gelu_tanh is z * sigmoid(p), p = 2 sqrt(2/pi) (z + 0.044715 z^3): (1 + tanh x) / 2 without its cancellation.
 constexpr float kGelu1 = 1.59576912f, kGelu3 = 0.0713548163f;
-__device__ __forceinline__ float gelu_p(float z) { return z * fmaf(kGelu3, z * z, kGelu1); }
-// The normal distribution's integral, without the cancellation of 1 + erf.
-__device__ __forceinline__ float normal(float z) { return 0.5f * erfcf(-0.707106781f * z); }
+__device__ __forceinline__ float gelu_sigmoid(float z) {
+    const float t = z * fmaf(-kGelu3 * kLog2E, z * z, -kGelu1 * kLog2E);
+    return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(t));
+}
+// The normal distribution's integral up to -|z|, and its density without the
+// factor 1 / sqrt(2 pi): e^(-z^2/2) times a polynomial in t = 1 / (1 + 0.34 |z|),
+// fitted to least relative error over |z| <= 14.5 (3.4e-8; in FP32 6 steps).
+// 1 + erf would cancel; erfcf takes five times as long.
+__device__ __forceinline__ float tail(float z, float &density) {
+    const float t = __builtin_amdgcn_rcpf(fmaf(0.34f, fabsf(z), 1.0f));
+    density = __builtin_amdgcn_exp2f(z * z * (-0.5f * kLog2E));
+    float p = -0.02587636187672615f;
+    p = fmaf(p, t, 0.1383567452430725f);
+    p = fmaf(p, t, -0.2708704173564911f);
+    p = fmaf(p, t, 0.1997169554233551f);
+    p = fmaf(p, t, -0.043105896562337875f);
+    p = fmaf(p, t, 0.11471346020698547f);
+    p = fmaf(p, t, 0.11535173654556274f);
+    p = fmaf(p, t, 0.13609223067760468f);
+    p = fmaf(p, t, 0.135621577501297f);
+    return p * t * density;
+}
 
-// f(z). at(-inf) = 0 and f(inf) = inf: clamped below, where z * 0 would be NaN.
+// f(z).
 template <int ACT> __device__ __forceinline__ float act_of(float z) {
     if constexpr (ACT == MI_ACT_RELU) return z <= 0.0f ? 0.0f : z;
     if constexpr (ACT == MI_ACT_SILU) return above(z) * sigmoid(z);
-    if constexpr (ACT == MI_ACT_GELU) return above(z) * normal(z);
-    if constexpr (ACT == MI_ACT_GELU_TANH) return above(z) * sigmoid(gelu_p(within(z)));
+    if constexpr (ACT == MI_ACT_GELU) {
+        // z (1 - tail) above 0 and z tail below it.
+        float density;
+        const float h = tail(z, density);
+        return fmaf(-fminf(fabsf(z), 104.0f), h, fmaxf(z, 0.0f));
+    }
+    if constexpr (ACT == MI_ACT_GELU_TANH) return above(z) * gelu_sigmoid(z);
     return z;
 }
 // f(z) and f'(z).
@@ -70,12 +94,12 @@ template <int ACT> __device__ __forceinline__ void act_both(float z, float &f, f
         f = above(z) * s;
         df = s * fmaf(within(z), 1.0f - s, 1.0f);
     } else if constexpr (ACT == MI_ACT_GELU) {
-        const float c = within(z), s = normal(z);
-        f = above(z) * s;
-        // c * c / 2 passes 104 from 14.4 on, where the density is below FP32's least number.
-        df = fmaf(c * 0.398942280f, exp_of(-(c * c > 208.0f ? 208.0f : c * c) * 0.5f), s);
+        float density;
+        const float h = tail(z, density), c = within(z);
+        f = fmaf(-fabsf(c), h, fmaxf(z, 0.0f));
+        df = fmaf(c * 0.398942280f, density, z > 0.0f ? 1.0f - h : h);
     } else if constexpr (ACT == MI_ACT_GELU_TANH) {
-        const float c = within(z), s = sigmoid(gelu_p(c));
+        const float c = within(z), s = gelu_sigmoid(z);
         f = above(z) * s;
         df = fmaf(c * fmaf(3.0f * kGelu3, c * c, kGelu1), s * (1.0f - s), s);
     } else {
@@ -155,11 +179,12 @@ __device__ __forceinline__ void put_out(const LinArgs &g, int m, int n, float (&
 
 inline bool is_half(int t) { return t == MI_BF16 || t == MI_F16; }
 
-// Tiles that go through LDS (linear_tile.h, one file for each type), and
+// Tiles that go through LDS (linear_tile.h, a file for each type), and
 // products of few rows without a barrier in their sum (linear_direct.hip).
 // `shape` names one of their tile shapes.
 int launch_tiles_bf16(bool gated, bool ta, bool tb, int shape, LinArgs &g, hipStream_t stream);
 int launch_tiles_f16(bool gated, bool ta, bool tb, int shape, LinArgs &g, hipStream_t stream);
+int launch_direct(int type, bool gated, int shape, LinArgs &g, hipStream_t stream);
 
 }  // namespace misgemm_linear
 

@@ -33,9 +33,90 @@ bool whole(const void *p, long long ld, bool kmajor, int across) {
     return aligned(p, 16) && ld % 8 == 0 && ld < 1 << 23 && (kmajor || across % 8 == 0);
 }
 
+// A kernel's time in us is taken to be
+//   first + round * (rounds - 1) + step * rounds * steps + share * steps * workgroups / 256
+// and, where k is split, split + part * splits more: a round is 256 workgroups
+// (one for each CU), a step a block of 64 values of k for each of a workgroup's
+// waves that split it. The constants are fitted to the measured times of all
+// kernels on 680 shapes (M, N and K from 1, 64 and 64 to 8192, all layouts and
+// alignments), which they reproduce to 5-14%; the kernel picked was 2.0% slower
+// than the fastest on average, 13% in one case of twenty, 42% at worst (176 x
+// 4586 x 5334, NN, rows 2 bytes aligned: 46 us for 32 with k split by four).
+struct Fit {
+    float first, round, step, share;
+};
+struct Cost {
+    int kernel, bm, bn, waves;
+    float split, part;
+    Fit fit[2];   // below 16: rows 16 bytes aligned; not. From 16 on: both operands with k running fastest; not
+};
+// 0 to 15 are linear_direct.hip's tile shapes, those from 16 on linear_tile.h's
+// (16 and 17 for any alignment, the others for whole 16 bytes).
+constexpr Cost kLinear[] = {
+    {0, 16, 16, 16, 0, 0, {{2.88f, 0.48f, 0.47f, 0.13f}, {2.5f, 0, 0.83f, 0.31f}}},
+    {1, 16, 32, 8, 0, 0, {{3.2f, 0.29f, 0.36f, 0.03f}, {2.84f, 0, 0.81f, 0}}},
+    {2, 32, 32, 8, 0, 0, {{3.16f, 0.44f, 0.52f, 0.02f}, {2.71f, 0, 1.03f, 0.18f}}},
+    {4, 64, 32, 4, 0, 0, {{3.51f, 0.07f, 0.51f, 0.08f}, {2.97f, 0, 0.94f, 0.14f}}},
+    {3, 48, 16, 8, 0, 0, {{3.03f, 0.25f, 0.54f, 0.02f}, {2.73f, 0, 0.8f, 0.47f}}},
+    {16, 128, 128, 1, 2.16f, 0.58f, {{4.55f, 1.59f, 0.59f, 0.37f}, {5.16f, 1.2f, 0.9f, 0}}},
+    {17, 64, 128, 1, 1.56f, 0.37f, {{3.76f, 0.55f, 0.43f, 0.15f}, {4.03f, 0.05f, 0.69f, 0}}},
+    {18, 64, 128, 1, 1.27f, 0.33f, {{4.02f, 1.5f, 0.25f, 0.16f}, {4.17f, 1.6f, 0.29f, 0.09f}}},
+    {19, 128, 128, 1, 1.72f, 0.58f, {{4.83f, 2.05f, 0.35f, 0.41f}, {5.26f, 3.26f, 0.38f, 0.31f}}},
+    {20, 128, 128, 1, 1.75f, 0.58f, {{5.13f, 4.6f, 0.36f, 0.26f}, {5.45f, 4.72f, 0.4f, 0.17f}}},
+    {21, 128, 256, 1, 2.58f, 1.13f, {{6.79f, 7.87f, 0.6f, 0.5f}, {7.33f, 8.55f, 0.64f, 0.32f}}},
+    {22, 256, 256, 1, 0, 0, {{9.91f, 6.82f, 0.98f, 0.94f}, {11.06f, 14.22f, 1, 0.42f}}},
+};
+constexpr Cost kGated[] = {
+    {0, 16, 16, 16, 0, 0, {{2.72f, 1.13f, 0.84f, 0.29f}, {1.84f, 0.44f, 1.82f, 0.13f}}},
+    {1, 16, 16, 8, 0, 0, {{2.99f, 0.16f, 0.41f, 0.11f}, {2.96f, 0.03f, 0.77f, 0.05f}}},
+    {2, 16, 32, 8, 0, 0, {{3.02f, 0.72f, 0.75f, 0.26f}, {2.33f, 0.11f, 1.52f, 0}}},
+    {3, 32, 16, 8, 0, 0, {{3.15f, 0.22f, 0.58f, 0.1f}, {2.71f, 0, 1.12f, 0}}},
+    {4, 64, 16, 4, 0, 0, {{3.3f, 0.13f, 0.54f, 0.1f}, {3.14f, 0.24f, 0.95f, 0}}},
+    {16, 128, 128, 1, 3.03f, 1.19f, {{5.54f, 4.89f, 0.92f, 0.73f}, {}}},
+    {17, 64, 128, 1, 2.28f, 0.67f, {{4.4f, 0.71f, 0.68f, 0.38f}, {}}},
+    {18, 64, 128, 1, 1.81f, 0.6f, {{4.43f, 3.87f, 0.45f, 0.3f}, {}}},
+    {19, 64, 128, 1, 1.94f, 0.6f, {{4.44f, 0.68f, 0.39f, 0.52f}, {}}},
+    {21, 128, 128, 1, 2.78f, 1.12f, {{5.82f, 5.02f, 0.62f, 0.59f}, {}}},
+    {22, 256, 128, 1, 0, 0, {{8.96f, 8.67f, 0.99f, 0.73f}, {}}},
+};
+
+// The kernel that is expected to be fastest, and how many workgroups share its k.
+int pick(LinArgs &g, bool gated, bool ta, bool tb) {
+    const Cost *costs = gated ? kGated : kLinear;
+    const int count = gated ? sizeof kGated / sizeof *kGated : sizeof kLinear / sizeof *kLinear;
+    const bool kmajor = !ta && tb;
+    const bool few = kmajor && g.zs == nullptr && g.K >= 8 && g.lda < 1 << 25 && g.ldb < 1 << 25 && g.ldu < 1 << 25;
+    const int kblocks = (g.K + kStep - 1) / kStep;
+    int best = 16;
+    float least = 3e38f;
+    g.splits = 1;
+    for (const Cost *c = costs; c < costs + count; ++c) {
+        const long long tiles = (g.M + c->bm - 1LL) / c->bm * ((g.N + c->bn - 1LL) / c->bn);
+        if (c->kernel < 16 ? !few || tiles * 64 * c->waves >= 1LL << 32 : c->kernel > 17 && !g.direct) continue;
+        const Fit &f = c->fit[c->kernel < 16 ? !g.direct : !kmajor];
+        // At least three blocks of k for each workgroup, and three workgroups to a CU at most.
+        for (int splits = 1; splits == 1 || (c->split > 0.0f && kblocks / splits >= 3 && tiles * splits <= 3 * kNumCus && splits <= 16); splits *= 2) {
+            const float groups = (float)(tiles * splits);
+            const float rounds = (float)((tiles * splits + kNumCus - 1) / kNumCus);
+            const int each = (kblocks + splits - 1) / splits;
+            const float steps = (float)((each + c->waves - 1) / c->waves);
+            const float us = f.first + f.round * (rounds - 1) + f.step * rounds * steps + f.share * steps * groups / kNumCus +
+                             (splits > 1 ? c->split + c->part * splits : 0.0f);
+            if (us < least) {
+                least = us;
+                best = c->kernel;
+                g.splits = splits;
+            }
+        }
+    }
+    return best;
+}
+
 int launch(int type, bool gated, bool ta, bool tb, LinArgs &g, hipStream_t stream) {
-    return type == MI_BF16 ? launch_tiles_bf16(gated, ta, tb, 0, g, stream)
-                           : launch_tiles_f16(gated, ta, tb, 0, g, stream);
+    const int kernel = pick(g, gated, ta, tb);
+    if (kernel < 16) return launch_direct(type, gated, kernel, g, stream);
+    return type == MI_BF16 ? launch_tiles_bf16(gated, ta, tb, kernel - 16, g, stream)
+                           : launch_tiles_f16(gated, ta, tb, kernel - 16, g, stream);
 }
 
 }  // namespace

@@ -25,6 +25,14 @@ __device__ __forceinline__ void meet() {
     __builtin_amdgcn_s_barrier();
     asm volatile("" ::: "memory");
 }
+// The same with each wave's last N loads to LDS left on their way.
+template <int N> __device__ __forceinline__ void meet_but() {
+    static_assert(N >= 0 && N < 64, "the counter's range");
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_waitcnt((N & 15) | N >> 4 << 14 | 7 << 4);   // none of the others
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+}
 
 template <class T> __device__ __forceinline__ f32x4 product(typename Vec<T>::x8 a, typename Vec<T>::x8 b, f32x4 c) {
     if constexpr (std::is_same<T, bf16>::value)
@@ -106,8 +114,10 @@ template <class T> struct Chunk {
 
 enum Way { DIRECT, STAGED };   // operands to LDS: without registers, or through them at any alignment
 
-template <class T, int BM, int BN, int WM, int WN, bool KA, bool KB, bool GATED, Way WAY>
-__global__ __launch_bounds__(64 * WM * WN, WM * WN == 8 ? 2 : BM * BN > 128 * 128 ? 1 : 2) void lin_tile(LinArgs g) {
+// BUFS blocks of k have room in LDS: one that is read, the others on their way.
+template <class T, int BM, int BN, int WM, int WN, int BUFS, bool KA, bool KB, bool GATED, Way WAY>
+__global__ __launch_bounds__(64 * WM * WN, WM * WN / 4 * (2 * BUFS * (BM + BN) * 128 <= 160 * 1024 ? 2 : 1)) void lin_tile(
+    LinArgs g) {
     constexpr int NT = 64 * WM * WN, TM = BM / WM, TN = BN / WN, MI = TM / 16, NI = TN / 16;
     static_assert(!GATED || (KB && BN == 256), "a tile has 128 columns of both projections");
     static_assert(TN == 64 || TN == 128, "");
@@ -117,7 +127,7 @@ __global__ __launch_bounds__(64 * WM * WN, WM * WN == 8 ? 2 : BM * BN > 128 * 12
     constexpr int BYTES = (BM + BN) * 128;
     // After the sums: 16 * ROWS rows of 64 outputs of each wave, and rows' maxima.
     constexpr int ROWS = MI < 4 ? MI : 4, TURN = WM * WN * ROWS * 16 * 64 * 4, MAXES = 4 * BM * WN * (GATED ? 2 : 1);
-    constexpr int LDS = 2 * BYTES > TURN + MAXES ? 2 * BYTES : TURN + MAXES;
+    constexpr int LDS = BUFS * BYTES > TURN + MAXES ? BUFS * BYTES : TURN + MAXES;
     __shared__ __align__(1024) uint8_t lds[LDS];
     const int tid = threadIdx.x, lane = tid % 64, wave = __builtin_amdgcn_readfirstlane(tid / 64);
     const int i = lane % 16, grp = lane / 16;
@@ -242,15 +252,22 @@ __global__ __launch_bounds__(64 * WM * WN, WM * WN == 8 ? 2 : BM * BN > 128 * 12
             h.a[p - NI] = PanelA::read(lds + buf * BYTES, at_a, p - NI, s);
     };
     constexpr int READS = MI + NI;
-    // The products of one half; before each row of them some of the next half's reads, and of `more`.
+    // The products of one half; before each row of them some of the next half's
+    // reads, and of `more`. Transposing reads are twice as many and spread over
+    // all rows, others over three quarters of them (each the faster, by 1 to 3%).
+    // Every other row goes backwards: one operand stays from product to product.
+    auto upto = [](int a) { return min(READS, KA && KB ? READS * a * 4 / (3 * MI) : READS * a / MI); };
     auto multiply = [&](int s, int next_buf, auto more) {
 #pragma unroll
         for (int a = 0; a < MI; ++a) {
 #pragma unroll
-            for (int p = READS * a / MI; p < READS * (a + 1) / MI; ++p) read(next_buf, s ^ 1, p);
+            for (int p = upto(a); p < upto(a + 1); ++p) read(next_buf, s ^ 1, p);
             more(a);
 #pragma unroll
-            for (int b = 0; b < NI; ++b) acc[a][b] = product<T>(half[s].b[b], half[s].a[a], acc[a][b]);
+            for (int b0 = 0; b0 < NI; ++b0) {
+                const int b = a & 1 ? NI - 1 - b0 : b0;
+                acc[a][b] = product<T>(half[s].b[b], half[s].a[a], acc[a][b]);
+            }
             __builtin_amdgcn_sched_barrier(0);
         }
     };
@@ -258,38 +275,58 @@ __global__ __launch_bounds__(64 * WM * WN, WM * WN == 8 ? 2 : BM * BN > 128 * 12
 
     const int last = WAY == STAGED ? kb1 : min(kb1, g.K / kStep);   // the blocks that the loop takes
     if (kb0 < last) {
+        constexpr int PER = PanelA::PER + PanelB::PER, AHEAD = BUFS - 1;
         Chunks w;
         if constexpr (WAY == STAGED) {
+            static_assert(BUFS == 2, "the third block on its way is in registers");
             fetch(w, kb0);
             write(w, kb0, 0);
             if (kb0 + 1 < last) fetch(w, kb0 + 1);
-        } else {
-            copy(kb0, 0);
-        }
-        meet();
-        if constexpr (WAY == STAGED) {
+            meet();
             if (kb0 + 1 < last) write(w, kb0 + 1, 1);
+            if (kb0 + 2 < last) fetch(w, kb0 + 2);
         } else {
-            if (kb0 + 1 < last) copy(kb0 + 1, 1);
+#pragma unroll
+            for (int k = 0; k < AHEAD; ++k)
+                if (kb0 + k < last) copy(kb0 + k, k);
+            if (kb0 + AHEAD <= last)
+                meet_but<PER *(AHEAD - 1)>();
+            else
+                meet();
+            if (kb0 + AHEAD < last) copy(kb0 + AHEAD, AHEAD);
         }
 #pragma unroll
         for (int p = 0; p < READS; ++p) read(0, 0, p);
+        int buf = 0;
 #pragma unroll 1
         for (int kb = kb0; kb < last; ++kb) {
-            const int buf = (kb - kb0) & 1;
-            if constexpr (WAY == STAGED) {
-                if (kb + 2 < last) fetch(w, kb + 2);
-            }
+            const int next = buf + 1 == BUFS ? 0 : buf + 1;
             multiply(0, buf, nothing);
             // All of this block is in registers, and the next one has landed.
-            meet();
             if constexpr (WAY == STAGED) {
+                meet();
                 if (kb + 2 < last) write(w, kb + 2, buf);
-                multiply(1, buf ^ 1, nothing);
+                if (kb + 3 < last) fetch(w, kb + 3);
+                multiply(1, next, nothing);
             } else {
-                if (kb + 2 < last) copy(kb + 2, buf);
-                multiply(1, buf ^ 1, nothing);
+                if (BUFS > 2 && kb + BUFS <= last)
+                    meet_but<PER *(BUFS - 2)>();
+                else
+                    meet();
+                // The block that this one's place is for, a part before each row of products.
+                const bool more = kb + BUFS < last;
+                multiply(1, next, [&](int a) {
+                    if (!more) return;
+#pragma unroll
+                    for (int j = PER * a / MI; j < PER * (a + 1) / MI; ++j) {
+                        if (j < PanelA::PER)
+                            copy_a(kb + BUFS, buf, j);
+                        else
+                            copy_b(kb + BUFS, buf, j - PanelA::PER);
+                    }
+                });
             }
+            buf = next;
         }
     }
     if constexpr (WAY == DIRECT) {
@@ -361,7 +398,8 @@ __global__ __launch_bounds__(64 * WM * WN, WM * WN == 8 ? 2 : BM * BN > 128 * 12
     constexpr int SHARE = GATED ? WN : 128 / TN;
     float *maxes = reinterpret_cast<float *>(lds + TURN);
     const bool in8 = g.zs != nullptr;
-    if (in8) {
+    auto row_maxes = [&](auto edge_) {
+        constexpr bool edge = decltype(edge_)::value;   // columns past the matrix do not count
 #pragma unroll
         for (int half = 0; half < (GATED ? 2 : 1); ++half)
 #pragma unroll
@@ -371,11 +409,32 @@ __global__ __launch_bounds__(64 * WM * WN, WM * WN == 8 ? 2 : BM * BN > 128 * 12
                 for (int b = half * NH; b < (half + 1) * NH; ++b)
 #pragma unroll
                     for (int j = 0; j < 4; ++j)
-                        m = fmaxf(m, n1 + 16 * (b - half * NH) + 4 * grp + j < g.N ? fabsf(acc[a][b][j]) : 0.0f);
+                        m = fmaxf(m, edge && n1 + 16 * (b - half * NH) + 4 * grp + j >= g.N ? 0.0f : fabsf(acc[a][b][j]));
                 m = fmaxf(m, __shfl_xor(m, 16));
                 m = fmaxf(m, __shfl_xor(m, 32));
                 if (grp == 0) maxes[(half * WN + wn) * BM + wm * TM + 16 * a + i] = m;
             }
+    };
+    if (in8) {
+        if (n0 + COLS > g.N)
+            row_maxes(std::true_type{});
+        else
+            row_maxes(std::false_type{});
+        __syncthreads();
+        // The tables, and what values are multiplied by in the maxima's place.
+        constexpr int EACH = WN / SHARE;   // blocks of 128 columns, or weights, times rows
+        const float most = g.ztype == MI_E4M3 ? top<MI_E4M3>() : top<MI_E5M2>();
+        for (int t = tid; t < (GATED ? 2 : EACH) * BM; t += NT) {
+            const int part = t / BM, r = t % BM, m = m0 + r, n = GATED ? n0 : n0 + kBlock * part;
+            float a = kTiny;
+#pragma unroll
+            for (int w = 0; w < SHARE; ++w) a = fmaxf(a, maxes[(part * SHARE + w) * BM + r]);
+            maxes[part * SHARE * BM + r] = most / a;
+            if (m < g.M && n < g.N) {
+                float *table = GATED && part == 1 ? g.zus : g.zs;
+                table[n / kBlock * (GATED && part == 1 ? g.ldsu : g.lds) + m] = a / most;
+            }
+        }
         __syncthreads();
     }
     // Outputs turn in LDS, each wave's in its own, and leave as whole rows:
@@ -411,22 +470,20 @@ __global__ __launch_bounds__(64 * WM * WN, WM * WN == 8 ? 2 : BM * BN > 128 * 12
                     }
                 }
                 if (in8 && m < g.M && n < g.N) {
-                    auto keep = [&](const float (&z)[8], int half, uint8_t *q, long long ldq, float *table, long long lds_) {
-                        float most = kTiny;
-#pragma unroll
-                        for (int w = 0; w < SHARE; ++w)
-                            most = fmaxf(most, maxes[(half * WN + wn / SHARE * SHARE + w) * BM + wm * TM + 16 * a0 + r]);
-                        const float top_ = g.ztype == MI_E4M3 ? top<MI_E4M3>() : top<MI_E5M2>(), f = top_ / most;
-                        const int words[2] = {
-                            g.ztype == MI_E4M3 ? pack4<MI_E4M3>(z[0] * f, z[1] * f, z[2] * f, z[3] * f)
-                                               : pack4<MI_E5M2>(z[0] * f, z[1] * f, z[2] * f, z[3] * f),
-                            g.ztype == MI_E4M3 ? pack4<MI_E4M3>(z[4] * f, z[5] * f, z[6] * f, z[7] * f)
-                                               : pack4<MI_E5M2>(z[4] * f, z[5] * f, z[6] * f, z[7] * f)};
-                        store_bytes<8>(q + m * ldq + n, g.N - n, words);
-                        if (n % kBlock == 0) table[n / kBlock * lds_ + m] = most / top_;
+                    auto keep = [&](const float (&z)[8], int part, void *q, long long ldq) {
+                        const float f = maxes[part * SHARE * BM + wm * TM + 16 * a0 + r];
+                        int w[2];
+                        if (g.ztype == MI_E4M3) {
+                            w[0] = pack4<MI_E4M3>(z[0] * f, z[1] * f, z[2] * f, z[3] * f);
+                            w[1] = pack4<MI_E4M3>(z[4] * f, z[5] * f, z[6] * f, z[7] * f);
+                        } else {
+                            w[0] = pack4<MI_E5M2>(z[0] * f, z[1] * f, z[2] * f, z[3] * f);
+                            w[1] = pack4<MI_E5M2>(z[4] * f, z[5] * f, z[6] * f, z[7] * f);
+                        }
+                        store_bytes<8>(static_cast<uint8_t *>(q) + m * ldq + n, g.N - n, w);
                     };
-                    keep(v, 0, static_cast<uint8_t *>(g.z), g.ldz, g.zs, g.lds);
-                    if constexpr (GATED) keep(u, 1, static_cast<uint8_t *>(g.zu), g.ldzu, g.zus, g.ldsu);
+                    keep(v, GATED ? 0 : wn / SHARE, g.z, g.ldz);
+                    if constexpr (GATED) keep(u, 1, g.zu, g.ldzu);
                 }
                 put_out<T, GATED, 8>(g, m, n, v, u);
             }
@@ -434,31 +491,48 @@ __global__ __launch_bounds__(64 * WM * WN, WM * WN == 8 ? 2 : BM * BN > 128 * 12
         }
 }
 
-template <class T, int BM, int BN, int WM, int WN, bool KA, bool KB, bool GATED, Way WAY>
-int launch_tile(LinArgs &g, bool split, hipStream_t stream) {
+template <class T, int BM, int BN, int WM, int WN, int BUFS, bool KA, bool KB, bool GATED, Way WAY>
+int launch_tile(LinArgs &g, hipStream_t stream) {
     constexpr int COLS = GATED ? BN / 2 : BN;
     g.tiles_m = (g.M + BM - 1) / BM;
     g.tiles_n = (g.N + COLS - 1) / COLS;
     const int kblocks = (g.K + kStep - 1) / kStep;
     const long long tiles = (long long)g.tiles_m * g.tiles_n;
-    g.splits = split ? splits_of(tiles, kblocks) : 1;
-    static_assert((size_t)2 * kNumCus * 64 * 256 <= misgemm_workspace::kFloats &&
-                  2 * kNumCus <= misgemm_workspace::kCounters, "partial tiles fit the workspace");
-    if (g.splits > 1 && !misgemm_workspace::get(stream, &g.ws, &g.counters)) g.splits = 1;
+    // What was chosen, where a tile's parts fit the workspace and there is one.
+    if (g.splits > 1 && (tiles * g.splits * BM * BN > (long long)misgemm_workspace::kFloats ||
+                         tiles > misgemm_workspace::kCounters || !misgemm_workspace::get(stream, &g.ws, &g.counters)))
+        g.splits = 1;
     g.kb_per_split = (kblocks + g.splits - 1) / g.splits;
-    hipLaunchKernelGGL((lin_tile<T, BM, BN, WM, WN, KA, KB, GATED, WAY>), dim3((unsigned)(tiles * g.splits)),
+    if (g.splits > 1) g.splits = (kblocks + g.kb_per_split - 1) / g.kb_per_split;
+    hipLaunchKernelGGL((lin_tile<T, BM, BN, WM, WN, BUFS, KA, KB, GATED, WAY>), dim3((unsigned)(tiles * g.splits)),
                        dim3(64 * WM * WN), 0, stream, g);
     return launched();
 }
 
 template <class T, bool KA, bool KB> int launch_linear(int shape, LinArgs &g, hipStream_t stream) {
     switch (shape) {
-        default: return launch_tile<T, 128, 128, 2, 2, KA, KB, false, STAGED>(g, true, stream);
+        case 0: return launch_tile<T, 128, 128, 4, 2, 2, KA, KB, false, STAGED>(g, stream);
+        case 1: return launch_tile<T, 64, 128, 4, 2, 2, KA, KB, false, STAGED>(g, stream);
+        case 2: return launch_tile<T, 64, 128, 4, 2, 3, KA, KB, false, DIRECT>(g, stream);
+        case 3: return launch_tile<T, 128, 128, 4, 2, 2, KA, KB, false, DIRECT>(g, stream);
+        case 4: return launch_tile<T, 128, 128, 4, 2, 4, KA, KB, false, DIRECT>(g, stream);
+        case 5: return launch_tile<T, 128, 256, 2, 4, 3, KA, KB, false, DIRECT>(g, stream);
+        case 6:
+            // Waves of 64 x 128 outputs, but of 128 x 64 where B alone comes by transposing reads.
+            if constexpr (KA && !KB) return launch_tile<T, 256, 256, 2, 4, 2, KA, KB, false, DIRECT>(g, stream);
+            return launch_tile<T, 256, 256, 4, 2, 2, KA, KB, false, DIRECT>(g, stream);
+        default: return MISGEMM_LAUNCH_FAILED;
     }
 }
 template <class T> int launch_gated(int shape, LinArgs &g, hipStream_t stream) {
     switch (shape) {
-        default: return launch_tile<T, 64, 256, 2, 2, true, true, true, STAGED>(g, true, stream);
+        case 0: return launch_tile<T, 128, 256, 2, 4, 2, true, true, true, STAGED>(g, stream);
+        case 1: return launch_tile<T, 64, 256, 2, 4, 2, true, true, true, STAGED>(g, stream);
+        case 2: return launch_tile<T, 64, 256, 2, 4, 3, true, true, true, DIRECT>(g, stream);
+        case 3: return launch_tile<T, 64, 256, 2, 4, 2, true, true, true, DIRECT>(g, stream);
+        case 5: return launch_tile<T, 128, 256, 2, 4, 3, true, true, true, DIRECT>(g, stream);
+        case 6: return launch_tile<T, 256, 256, 4, 2, 2, true, true, true, DIRECT>(g, stream);
+        default: return MISGEMM_LAUNCH_FAILED;
     }
 }
 
