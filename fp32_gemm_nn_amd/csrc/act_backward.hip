@@ -3,6 +3,8 @@
 // matrices), their gradients, f(z) or f(g) u again, and the sums over rows
 // that are the biases' gradients.
 
+#include <type_traits>
+
 #include "linear.h"
 
 namespace {
@@ -22,38 +24,63 @@ struct BackArgs {
 
 constexpr int kNone = 0;   // Z: a matrix of the gradients' type, not an 8-bit one
 
-// Eight values of a checkpoint.
-template <class T, int FMT>
-__device__ __forceinline__ void load_kept(const void *base, long long at, int n, float scale, float (&v)[8]) {
-    if constexpr (FMT == kNone) {
-        load8(static_cast<const T *>(base) + at, n, v);
-    } else {
+// Eight 8-bit values as Eight has them of other types: one read without a
+// branch, of the row's last eight where it ends, moved to their place.
+struct Eight8 {
+    i32x2 v;
+    __device__ __forceinline__ void fetch(const uint8_t *row, int col, int cols) {
         typedef int words __attribute__((ext_vector_type(2), aligned(1)));
-        const uint8_t *p = static_cast<const uint8_t *>(base) + at;
-        i32x2 w = {0, 0};
-        if (n >= 8) {
-            w = *reinterpret_cast<const words *>(p);
+        v = *reinterpret_cast<const words *>(row + min(col, cols - 8));
+    }
+    __device__ __forceinline__ void settle(int col, int cols) {
+        const int over = max(col - (cols - 8), 0);
+        unsigned long long w = (uint32_t)v[0] | (unsigned long long)(uint32_t)v[1] << 32;
+        w = over < 8 ? w >> (8 * over) : 0;
+        v = i32x2{(int)w, (int)(w >> 32)};
+    }
+};
+
+// Eight values of a row of `cols` from column col on, in T or (FMT) in 8 bits.
+template <class T, int FMT> struct Row8 {
+    typename std::conditional<FMT == kNone, Eight<T, false>, Eight8>::type w;
+    using Memory = typename std::conditional<FMT == kNone, T, uint8_t>::type;
+    __device__ __forceinline__ void fetch(const void *base, long long row, int col, int cols) {
+        const Memory *p = static_cast<const Memory *>(base) + row;
+        if (cols >= 8) {
+            w.fetch(p, col, cols);
+        } else if constexpr (FMT == kNone) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) w.v[j] = j < cols ? p[j] : static_cast<T>(0.0f);
         } else {
+            w.v = i32x2{0, 0};
 #pragma unroll
             for (int j = 0; j < 8; ++j)
-                if (j < n) w[j / 4] |= (int)((uint32_t)p[j] << (8 * (j % 4)));
+                if (j < cols) w.v[j / 4] |= (int)((uint32_t)p[j] << (8 * (j % 4)));
         }
+    }
+    __device__ __forceinline__ void values(int col, int cols, float scale, float (&v)[8]) {
+        if (cols >= 8 && col > cols - 8) w.settle(col, cols);
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            if constexpr (FMT == MI_E4M3) {
-                v[4 * h] = __builtin_amdgcn_cvt_f32_fp8(w[h], 0) * scale;
-                v[4 * h + 1] = __builtin_amdgcn_cvt_f32_fp8(w[h], 1) * scale;
-                v[4 * h + 2] = __builtin_amdgcn_cvt_f32_fp8(w[h], 2) * scale;
-                v[4 * h + 3] = __builtin_amdgcn_cvt_f32_fp8(w[h], 3) * scale;
-            } else {
-                v[4 * h] = __builtin_amdgcn_cvt_f32_bf8(w[h], 0) * scale;
-                v[4 * h + 1] = __builtin_amdgcn_cvt_f32_bf8(w[h], 1) * scale;
-                v[4 * h + 2] = __builtin_amdgcn_cvt_f32_bf8(w[h], 2) * scale;
-                v[4 * h + 3] = __builtin_amdgcn_cvt_f32_bf8(w[h], 3) * scale;
+        for (int j = 0; j < 8; ++j) {
+            if constexpr (FMT == kNone) v[j] = static_cast<float>(w.v[j]);
+        }
+        if constexpr (FMT == MI_E4M3 || FMT == MI_E5M2) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                v[4 * h] = value<0>(w.v[h]) * scale;
+                v[4 * h + 1] = value<1>(w.v[h]) * scale;
+                v[4 * h + 2] = value<2>(w.v[h]) * scale;
+                v[4 * h + 3] = value<3>(w.v[h]) * scale;
             }
         }
     }
-}
+    template <int I> static __device__ __forceinline__ float value(int w) {
+        if constexpr (FMT == MI_E4M3)
+            return __builtin_amdgcn_cvt_f32_fp8(w, I);
+        else
+            return __builtin_amdgcn_cvt_f32_bf8(w, I);
+    }
+};
 
 constexpr int kLanes = 16, kRows = 16, kCols = kLanes * 8;   // of a workgroup: threads of a row, rows, columns
 
@@ -63,30 +90,49 @@ template <class T, int FMT, int ACT, bool GATED> __global__ __launch_bounds__(25
     const int col = strip * kCols + tx * 8, n = a.cols - col;
     const long long r0 = (long long)chunk * a.chunk_rows;
     const int end = (int)(r0 + a.chunk_rows < a.rows ? r0 + a.chunk_rows : a.rows);
+    constexpr int AHEAD = GATED ? 2 : 1;
     float sz[8] = {}, su[8] = {};
     if (n > 0) {
-        for (long long row = r0 + ty; row < end; row += kRows) {
-            float dy[8], z[8], u[8], f[8], dz[8], du[8];
-            load8(static_cast<const T *>(a.dy) + row * a.lddy + col, n, dy);
-            load_kept<T, FMT>(a.z, row * a.ldz + col, n, FMT == kNone ? 1.0f : a.zs[strip * a.lds + row], z);
-            if constexpr (GATED) load_kept<T, FMT>(a.u, row * a.ldu + col, n, FMT == kNone ? 1.0f : a.us[strip * a.ldsu + row], u);
+        // AHEAD rows' reads on their way at once; past the end the last one's, for nothing.
+        for (long long first = r0 + ty; first < end; first += kRows * AHEAD) {
+            Row8<T, kNone> dyr[AHEAD];
+            Row8<T, FMT> zr[AHEAD], ur[AHEAD];
+            float zs[AHEAD], us[AHEAD];
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                float df;
-                act_both<ACT>(z[j], f[j], df);
-                if constexpr (GATED) {
-                    du[j] = dy[j] * f[j];
-                    dz[j] = dy[j] * u[j] * df;
-                    f[j] *= u[j];
-                    su[j] += du[j];
-                } else {
-                    dz[j] = dy[j] * df;
-                }
-                sz[j] += dz[j];
+            for (int i = 0; i < AHEAD; ++i) {
+                const long long at = first + i * kRows, row = at < end ? at : end - 1;
+                dyr[i].fetch(a.dy, row * a.lddy, col, a.cols);
+                zr[i].fetch(a.z, row * a.ldz, col, a.cols);
+                if constexpr (GATED) ur[i].fetch(a.u, row * a.ldu, col, a.cols);
+                zs[i] = FMT == kNone ? 1.0f : a.zs[strip * a.lds + row];
+                us[i] = FMT == kNone || !GATED ? 1.0f : a.us[strip * a.ldsu + row];
             }
-            store8(static_cast<T *>(a.dz) + row * a.lddz + col, n, dz);
-            if constexpr (GATED) store8(static_cast<T *>(a.du) + row * a.lddu + col, n, du);
-            if (a.y != nullptr) store8(static_cast<T *>(a.y) + row * a.ldy + col, n, f);
+#pragma unroll
+            for (int i = 0; i < AHEAD; ++i) {
+                const long long row = first + i * kRows;
+                if (row >= end) break;
+                float dy[8], z[8], u[8], f[8], dz[8], du[8];
+                dyr[i].values(col, a.cols, 1.0f, dy);
+                zr[i].values(col, a.cols, zs[i], z);
+                if constexpr (GATED) ur[i].values(col, a.cols, us[i], u);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    float df;
+                    act_both<ACT>(z[j], f[j], df);
+                    if constexpr (GATED) {
+                        du[j] = dy[j] * f[j];
+                        dz[j] = dy[j] * u[j] * df;
+                        f[j] *= u[j];
+                        su[j] += du[j];
+                    } else {
+                        dz[j] = dy[j] * df;
+                    }
+                    sz[j] += dz[j];
+                }
+                store8(static_cast<T *>(a.dz) + row * a.lddz + col, n, dz);
+                if constexpr (GATED) store8(static_cast<T *>(a.du) + row * a.lddu + col, n, du);
+                if (a.y != nullptr) store8(static_cast<T *>(a.y) + row * a.ldy + col, n, f);
+            }
         }
     }
     if (a.dbz == nullptr && a.dbu == nullptr) return;
@@ -124,9 +170,17 @@ template <class T, int FMT, int ACT, bool GATED> __global__ __launch_bounds__(25
         if (!is_last) return;
         if (threadIdx.x == 0) __hip_atomic_store(&a.counters[strip], 0, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
         if (mine) {
+            // Sixteen reads on their way at once; those past the last are not added.
             sum = 0.0f;
-            for (int k = 0; k < a.chunks; ++k)
-                sum += __hip_atomic_load(mid + (long long)k * a.cols, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+            for (int k0 = 0; k0 < a.chunks; k0 += 16) {
+                float v[16];
+#pragma unroll
+                for (int k = 0; k < 16; ++k)
+                    v[k] = __hip_atomic_load(mid + (long long)min(k0 + k, a.chunks - 1) * a.cols, __ATOMIC_RELAXED,
+                                             __HIP_MEMORY_SCOPE_AGENT);
+#pragma unroll
+                for (int k = 0; k < 16; ++k) sum += k0 + k < a.chunks ? v[k] : 0.0f;
+            }
         }
     }
     if (mine) out[at] = a.beta == 0.0f ? sum : fmaf(a.beta, out[at], sum);

@@ -38,7 +38,7 @@ bool whole(const void *p, long long ld, bool kmajor, int across) {
 // and, where k is split, split + part * splits more: a round is 256 workgroups
 // (one for each CU), a step a block of 64 values of k for each of a workgroup's
 // waves that split it. The constants are fitted to the measured times of all
-// kernels on 680 shapes (M, N and K from 1, 64 and 64 to 8192, all layouts and
+// kernels on 980 shapes (M, N and K from 1, 64 and 64 to 8192, all layouts and
 // alignments), which they reproduce to 5-14%; the kernel picked was 2.0% slower
 // than the fastest on average, 13% in one case of twenty, 42% at worst (176 x
 // 4586 x 5334, NN, rows 2 bytes aligned: 46 us for 32 with k split by four).
@@ -56,8 +56,8 @@ constexpr Cost kLinear[] = {
     {0, 16, 16, 16, 0, 0, {{2.88f, 0.48f, 0.47f, 0.13f}, {2.5f, 0, 0.83f, 0.31f}}},
     {1, 16, 32, 8, 0, 0, {{3.2f, 0.29f, 0.36f, 0.03f}, {2.84f, 0, 0.81f, 0}}},
     {2, 32, 32, 8, 0, 0, {{3.16f, 0.44f, 0.52f, 0.02f}, {2.71f, 0, 1.03f, 0.18f}}},
-    {4, 64, 32, 4, 0, 0, {{3.51f, 0.07f, 0.51f, 0.08f}, {2.97f, 0, 0.94f, 0.14f}}},
     {3, 48, 16, 8, 0, 0, {{3.03f, 0.25f, 0.54f, 0.02f}, {2.73f, 0, 0.8f, 0.47f}}},
+    {4, 64, 32, 4, 0, 0, {{3.51f, 0.07f, 0.51f, 0.08f}, {2.97f, 0, 0.94f, 0.14f}}},
     {16, 128, 128, 1, 2.16f, 0.58f, {{4.55f, 1.59f, 0.59f, 0.37f}, {5.16f, 1.2f, 0.9f, 0}}},
     {17, 64, 128, 1, 1.56f, 0.37f, {{3.76f, 0.55f, 0.43f, 0.15f}, {4.03f, 0.05f, 0.69f, 0}}},
     {18, 64, 128, 1, 1.27f, 0.33f, {{4.02f, 1.5f, 0.25f, 0.16f}, {4.17f, 1.6f, 0.29f, 0.09f}}},
@@ -67,17 +67,19 @@ constexpr Cost kLinear[] = {
     {22, 256, 256, 1, 0, 0, {{9.91f, 6.82f, 0.98f, 0.94f}, {11.06f, 14.22f, 1, 0.42f}}},
 };
 constexpr Cost kGated[] = {
-    {0, 16, 16, 16, 0, 0, {{2.72f, 1.13f, 0.84f, 0.29f}, {1.84f, 0.44f, 1.82f, 0.13f}}},
-    {1, 16, 16, 8, 0, 0, {{2.99f, 0.16f, 0.41f, 0.11f}, {2.96f, 0.03f, 0.77f, 0.05f}}},
-    {2, 16, 32, 8, 0, 0, {{3.02f, 0.72f, 0.75f, 0.26f}, {2.33f, 0.11f, 1.52f, 0}}},
-    {3, 32, 16, 8, 0, 0, {{3.15f, 0.22f, 0.58f, 0.1f}, {2.71f, 0, 1.12f, 0}}},
-    {4, 64, 16, 4, 0, 0, {{3.3f, 0.13f, 0.54f, 0.1f}, {3.14f, 0.24f, 0.95f, 0}}},
-    {16, 128, 128, 1, 3.03f, 1.19f, {{5.54f, 4.89f, 0.92f, 0.73f}, {}}},
-    {17, 64, 128, 1, 2.28f, 0.67f, {{4.4f, 0.71f, 0.68f, 0.38f}, {}}},
-    {18, 64, 128, 1, 1.81f, 0.6f, {{4.43f, 3.87f, 0.45f, 0.3f}, {}}},
-    {19, 64, 128, 1, 1.94f, 0.6f, {{4.44f, 0.68f, 0.39f, 0.52f}, {}}},
-    {21, 128, 128, 1, 2.78f, 1.12f, {{5.82f, 5.02f, 0.62f, 0.59f}, {}}},
-    {22, 256, 128, 1, 0, 0, {{8.96f, 8.67f, 0.99f, 0.73f}, {}}},
+    {0, 16, 16, 16, 0, 0, {{2.66f, 1.03f, 0.85f, 0.33f}, {1.8f, 0.26f, 1.71f, 0.3f}}},
+    {1, 16, 16, 8, 0, 0, {{3.12f, 0.09f, 0.38f, 0.12f}, {2.73f, 0, 0.79f, 0}}},
+    {2, 16, 32, 8, 0, 0, {{2.95f, 0.3f, 0.73f, 0.27f}, {2.23f, 0, 1.49f, 0.01f}}},
+    {3, 32, 16, 8, 0, 0, {{3.06f, 0.01f, 0.58f, 0.13f}, {2.44f, 0, 1.13f, 0}}},
+    {4, 64, 16, 4, 0, 0, {{3.32f, 0.02f, 0.55f, 0.07f}, {2.89f, 0, 1.01f, 0}}},
+    {16, 128, 128, 1, 3.06f, 1.21f, {{5.42f, 5.06f, 0.91f, 0.72f}, {}}},
+    {17, 64, 128, 1, 2.23f, 0.65f, {{4.41f, 0.78f, 0.67f, 0.43f}, {}}},
+    {18, 64, 128, 1, 1.75f, 0.64f, {{4.53f, 3.99f, 0.45f, 0.31f}, {}}},
+    {19, 64, 128, 1, 1.94f, 0.64f, {{4.49f, 0.75f, 0.39f, 0.56f}, {}}},
+    {20, 128, 64, 1, 1.89f, 0.65f, {{4.56f, 4.68f, 0.37f, 0.18f}, {}}},
+    {21, 128, 128, 1, 2.82f, 1.18f, {{5.87f, 5.9f, 0.61f, 0.48f}, {}}},
+    {22, 256, 128, 1, 0, 0, {{8.27f, 9.64f, 1, 0.63f}, {}}},
+    {23, 128, 64, 1, 1.94f, 0.6f, {{4.29f, 1.09f, 0.35f, 0.45f}, {}}},
 };
 
 // The kernel that is expected to be fastest, and how many workgroups share its k.
@@ -93,6 +95,7 @@ int pick(LinArgs &g, bool gated, bool ta, bool tb) {
     for (const Cost *c = costs; c < costs + count; ++c) {
         const long long tiles = (g.M + c->bm - 1LL) / c->bm * ((g.N + c->bn - 1LL) / c->bn);
         if (c->kernel < 16 ? !few || tiles * 64 * c->waves >= 1LL << 32 : c->kernel > 17 && !g.direct) continue;
+        if (gated && g.zs != nullptr && c->bn < kBlock) continue;   // a scale's columns are in one workgroup
         const Fit &f = c->fit[c->kernel < 16 ? !g.direct : !kmajor];
         // At least three blocks of k for each workgroup, and three workgroups to a CU at most.
         for (int splits = 1; splits == 1 || (c->split > 0.0f && kblocks / splits >= 3 && tiles * splits <= 3 * kNumCus && splits <= 16); splits *= 2) {

@@ -119,7 +119,7 @@ template <class T, int BM, int BN, int WM, int WN, int BUFS, bool KA, bool KB, b
 __global__ __launch_bounds__(64 * WM * WN, WM * WN / 4 * (2 * BUFS * (BM + BN) * 128 <= 160 * 1024 ? 2 : 1)) void lin_tile(
     LinArgs g) {
     constexpr int NT = 64 * WM * WN, TM = BM / WM, TN = BN / WN, MI = TM / 16, NI = TN / 16;
-    static_assert(!GATED || (KB && BN == 256), "a tile has 128 columns of both projections");
+    static_assert(!GATED || (KB && BN <= 256), "a tile has up to 128 columns of both projections");
     static_assert(TN == 64 || TN == 128, "");
     using PanelA = Panel<T, BM, NT, KA>;
     using PanelB = Panel<T, BN, NT, KB>;
@@ -530,7 +530,9 @@ template <class T> int launch_gated(int shape, LinArgs &g, hipStream_t stream) {
         case 1: return launch_tile<T, 64, 256, 2, 4, 2, true, true, true, STAGED>(g, stream);
         case 2: return launch_tile<T, 64, 256, 2, 4, 3, true, true, true, DIRECT>(g, stream);
         case 3: return launch_tile<T, 64, 256, 2, 4, 2, true, true, true, DIRECT>(g, stream);
+        case 4: return launch_tile<T, 128, 128, 4, 2, 4, true, true, true, DIRECT>(g, stream);
         case 5: return launch_tile<T, 128, 256, 2, 4, 3, true, true, true, DIRECT>(g, stream);
+        case 7: return launch_tile<T, 128, 128, 4, 2, 2, true, true, true, DIRECT>(g, stream);
         case 6: return launch_tile<T, 256, 256, 4, 2, 2, true, true, true, DIRECT>(g, stream);
         default: return MISGEMM_LAUNCH_FAILED;
     }
