@@ -30,6 +30,7 @@ struct LinArgs {
     int act, ztype;
     bool bias32, c32;             // FP32 rather than the operands' type
     bool direct;                  // whole aligned 16 bytes everywhere: copied to LDS without registers
+    bool near;                    // 32-bit offsets inside a tile, and rows of eight values at least
 };
 
 // f in few instructions: an epilogue forms 128 of them a lane while the matrix

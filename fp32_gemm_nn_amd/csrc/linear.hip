@@ -38,10 +38,10 @@ bool whole(const void *p, long long ld, bool kmajor, int across) {
 // and, where k is split, split + part * splits more: a round is 256 workgroups
 // (one for each CU), a step a block of 64 values of k for each of a workgroup's
 // waves that split it. The constants are fitted to the measured times of all
-// kernels on 980 shapes (M, N and K from 1, 64 and 64 to 8192, all layouts and
-// alignments), which they reproduce to 5-14%; the kernel picked was 2.0% slower
-// than the fastest on average, 13% in one case of twenty, 42% at worst (176 x
-// 4586 x 5334, NN, rows 2 bytes aligned: 46 us for 32 with k split by four).
+// kernels on 1000 shapes (M, N and K from 1, 64 and 64 to 8192, all layouts and
+// alignments), which they reproduce to 5-19%; the kernel picked was 1.6% slower
+// than the fastest on average, 9% in one case of twenty, 36% at worst (the gated
+// 3460 x 80 x 944: 17.4 us with k split by four, 12.8 in another tile).
 struct Fit {
     float first, round, step, share;
 };
@@ -51,35 +51,36 @@ struct Cost {
     Fit fit[2];   // below 16: rows 16 bytes aligned; not. From 16 on: both operands with k running fastest; not
 };
 // 0 to 15 are linear_direct.hip's tile shapes, those from 16 on linear_tile.h's
-// (16 and 17 for any alignment, the others for whole 16 bytes).
+// (below 24 for any alignment, the others for whole 16 bytes).
 constexpr Cost kLinear[] = {
-    {0, 16, 16, 16, 0, 0, {{2.88f, 0.48f, 0.47f, 0.13f}, {2.5f, 0, 0.83f, 0.31f}}},
-    {1, 16, 32, 8, 0, 0, {{3.2f, 0.29f, 0.36f, 0.03f}, {2.84f, 0, 0.81f, 0}}},
-    {2, 32, 32, 8, 0, 0, {{3.16f, 0.44f, 0.52f, 0.02f}, {2.71f, 0, 1.03f, 0.18f}}},
-    {3, 48, 16, 8, 0, 0, {{3.03f, 0.25f, 0.54f, 0.02f}, {2.73f, 0, 0.8f, 0.47f}}},
-    {4, 64, 32, 4, 0, 0, {{3.51f, 0.07f, 0.51f, 0.08f}, {2.97f, 0, 0.94f, 0.14f}}},
-    {16, 128, 128, 1, 2.16f, 0.58f, {{4.55f, 1.59f, 0.59f, 0.37f}, {5.16f, 1.2f, 0.9f, 0}}},
-    {17, 64, 128, 1, 1.56f, 0.37f, {{3.76f, 0.55f, 0.43f, 0.15f}, {4.03f, 0.05f, 0.69f, 0}}},
-    {18, 64, 128, 1, 1.27f, 0.33f, {{4.02f, 1.5f, 0.25f, 0.16f}, {4.17f, 1.6f, 0.29f, 0.09f}}},
-    {19, 128, 128, 1, 1.72f, 0.58f, {{4.83f, 2.05f, 0.35f, 0.41f}, {5.26f, 3.26f, 0.38f, 0.31f}}},
-    {20, 128, 128, 1, 1.75f, 0.58f, {{5.13f, 4.6f, 0.36f, 0.26f}, {5.45f, 4.72f, 0.4f, 0.17f}}},
-    {21, 128, 256, 1, 2.58f, 1.13f, {{6.79f, 7.87f, 0.6f, 0.5f}, {7.33f, 8.55f, 0.64f, 0.32f}}},
-    {22, 256, 256, 1, 0, 0, {{9.91f, 6.82f, 0.98f, 0.94f}, {11.06f, 14.22f, 1, 0.42f}}},
+    {0, 16, 16, 16, 0, 0, {{2.93f, 0.41f, 0.43f, 0.24f}, {2.4f, 0.08f, 1.02f, 0.09f}}},
+    {1, 16, 32, 8, 0, 0, {{3.11f, 0.26f, 0.37f, 0.1f}, {2.8f, 0, 0.77f, 0.02f}}},
+    {2, 32, 32, 8, 0, 0, {{3.07f, 0.37f, 0.54f, 0.05f}, {2.63f, 0, 1.08f, 0.06f}}},
+    {3, 48, 16, 8, 0, 0, {{3, 0.08f, 0.55f, 0.06f}, {2.64f, 0, 1.07f, 0}}},
+    {4, 64, 32, 4, 0, 0, {{3.43f, 0, 0.51f, 0.1f}, {2.91f, 0, 0.94f, 0}}},
+    {16, 128, 128, 1, 1.92f, 0.63f, {{4.45f, 2.22f, 0.47f, 0.31f}, {4.83f, 1.47f, 0.77f, 0}}},
+    {17, 64, 128, 1, 1.43f, 0.41f, {{3.71f, 1.03f, 0.36f, 0.19f}, {4.38f, 0.82f, 0.51f, 0}}},
+    {18, 256, 128, 1, 3.01f, 1.16f, {{6.13f, 6.81f, 0.78f, 0.5f}, {6.57f, 4.87f, 0.99f, 0.56f}}},
+    {24, 64, 128, 1, 1.2f, 0.36f, {{3.88f, 1.21f, 0.26f, 0.2f}, {4.12f, 1.55f, 0.3f, 0.07f}}},
+    {25, 128, 128, 1, 1.78f, 0.59f, {{4.53f, 1.47f, 0.35f, 0.57f}, {4.96f, 1.54f, 0.4f, 0.35f}}},
+    {26, 128, 128, 1, 1.72f, 0.61f, {{4.96f, 4.56f, 0.37f, 0.3f}, {5.11f, 4.87f, 0.42f, 0.16f}}},
+    {27, 128, 256, 1, 2.42f, 1.14f, {{6.5f, 7.02f, 0.6f, 0.64f}, {6.58f, 7.18f, 0.66f, 0.42f}}},
+    {28, 256, 256, 1, 0, 0, {{9.28f, 13.97f, 0.98f, 0.98f}, {9.86f, 18.23f, 1.04f, 0.63f}}},
 };
 constexpr Cost kGated[] = {
-    {0, 16, 16, 16, 0, 0, {{2.66f, 1.03f, 0.85f, 0.33f}, {1.8f, 0.26f, 1.71f, 0.3f}}},
-    {1, 16, 16, 8, 0, 0, {{3.12f, 0.09f, 0.38f, 0.12f}, {2.73f, 0, 0.79f, 0}}},
-    {2, 16, 32, 8, 0, 0, {{2.95f, 0.3f, 0.73f, 0.27f}, {2.23f, 0, 1.49f, 0.01f}}},
-    {3, 32, 16, 8, 0, 0, {{3.06f, 0.01f, 0.58f, 0.13f}, {2.44f, 0, 1.13f, 0}}},
-    {4, 64, 16, 4, 0, 0, {{3.32f, 0.02f, 0.55f, 0.07f}, {2.89f, 0, 1.01f, 0}}},
-    {16, 128, 128, 1, 3.06f, 1.21f, {{5.42f, 5.06f, 0.91f, 0.72f}, {}}},
-    {17, 64, 128, 1, 2.23f, 0.65f, {{4.41f, 0.78f, 0.67f, 0.43f}, {}}},
-    {18, 64, 128, 1, 1.75f, 0.64f, {{4.53f, 3.99f, 0.45f, 0.31f}, {}}},
-    {19, 64, 128, 1, 1.94f, 0.64f, {{4.49f, 0.75f, 0.39f, 0.56f}, {}}},
-    {20, 128, 64, 1, 1.89f, 0.65f, {{4.56f, 4.68f, 0.37f, 0.18f}, {}}},
-    {21, 128, 128, 1, 2.82f, 1.18f, {{5.87f, 5.9f, 0.61f, 0.48f}, {}}},
-    {22, 256, 128, 1, 0, 0, {{8.27f, 9.64f, 1, 0.63f}, {}}},
-    {23, 128, 64, 1, 1.94f, 0.6f, {{4.29f, 1.09f, 0.35f, 0.45f}, {}}},
+    {0, 16, 16, 16, 0, 0, {{2.69f, 0.93f, 0.83f, 0.49f}, {1.84f, 0.55f, 1.82f, 0.07f}}},
+    {1, 16, 16, 8, 0, 0, {{3.23f, 0, 0.36f, 0.2f}, {2.91f, 0, 0.77f, 0.02f}}},
+    {2, 16, 32, 8, 0, 0, {{2.95f, 0.14f, 0.72f, 0.41f}, {2.24f, 0, 1.56f, 0}}},
+    {3, 32, 16, 8, 0, 0, {{3.08f, 0, 0.58f, 0.15f}, {2.61f, 0, 1.11f, 0}}},
+    {4, 64, 16, 4, 0, 0, {{3.28f, 0.42f, 0.54f, 0.06f}, {2.86f, 0.09f, 1.01f, 0}}},
+    {16, 128, 128, 1, 3.13f, 1.18f, {{5.93f, 7.01f, 0.78f, 0.41f}, {}}},
+    {17, 64, 128, 1, 1.96f, 0.65f, {{4.43f, 1.81f, 0.53f, 0.31f}, {}}},
+    {24, 64, 128, 1, 1.92f, 0.6f, {{4.43f, 3.81f, 0.45f, 0.34f}, {}}},
+    {25, 64, 128, 1, 2, 0.62f, {{4.39f, 0.62f, 0.4f, 0.59f}, {}}},
+    {26, 128, 64, 1, 1.81f, 0.63f, {{4.42f, 4.17f, 0.36f, 0.23f}, {}}},
+    {27, 128, 64, 1, 1.78f, 0.65f, {{4.15f, 1.19f, 0.35f, 0.39f}, {}}},
+    {28, 128, 128, 1, 2.98f, 1.14f, {{5.8f, 6.87f, 0.61f, 0.41f}, {}}},
+    {29, 256, 128, 1, 0, 0, {{8.06f, 10, 0.99f, 0.67f}, {}}},
 };
 
 // The kernel that is expected to be fastest, and how many workgroups share its k.
@@ -94,17 +95,20 @@ int pick(LinArgs &g, bool gated, bool ta, bool tb) {
     g.splits = 1;
     for (const Cost *c = costs; c < costs + count; ++c) {
         const long long tiles = (g.M + c->bm - 1LL) / c->bm * ((g.N + c->bn - 1LL) / c->bn);
-        if (c->kernel < 16 ? !few || tiles * 64 * c->waves >= 1LL << 32 : c->kernel > 17 && !g.direct) continue;
+        if (c->kernel < 16 ? !few || tiles * 64 * c->waves >= 1LL << 32 : c->kernel >= 24 ? !g.direct : c->kernel > 16 && !g.near) continue;
         if (gated && g.zs != nullptr && c->bn < kBlock) continue;   // a scale's columns are in one workgroup
         const Fit &f = c->fit[c->kernel < 16 ? !g.direct : !kmajor];
         // At least three blocks of k for each workgroup, and three workgroups to a CU at most.
-        for (int splits = 1; splits == 1 || (c->split > 0.0f && kblocks / splits >= 3 && tiles * splits <= 3 * kNumCus && splits <= 16); splits *= 2) {
+        auto shared = [&](int splits) {
+            return c->split > 0.0f && splits <= 16 && kblocks / splits >= 3 && tiles * splits <= 3 * kNumCus;
+        };
+        for (int splits = 1; splits == 1 || shared(splits); splits *= 2) {
             const float groups = (float)(tiles * splits);
             const float rounds = (float)((tiles * splits + kNumCus - 1) / kNumCus);
             const int each = (kblocks + splits - 1) / splits;
             const float steps = (float)((each + c->waves - 1) / c->waves);
-            const float us = f.first + f.round * (rounds - 1) + f.step * rounds * steps + f.share * steps * groups / kNumCus +
-                             (splits > 1 ? c->split + c->part * splits : 0.0f);
+            float us = f.first + f.round * (rounds - 1) + f.step * rounds * steps + f.share * steps * groups / kNumCus;
+            if (splits > 1) us += c->split + c->part * splits;
             if (us < least) {
                 least = us;
                 best = c->kernel;
@@ -181,6 +185,7 @@ extern "C" int mi_linear(char transA, char transB, int type, int M, int N, int K
     g.act = act;
     g.ztype = ztype;
     g.direct = whole(A, lda, !ta, M) && whole(B, ldb, tb, N);
+    g.near = lda < 1 << 23 && ldb < 1 << 23 && (ta ? M : K) >= 8 && (tb ? K : N) >= 8;
     return launch(type, false, ta, tb, g, stream);
 }
 
@@ -246,5 +251,6 @@ extern "C" int mi_gated(int type, int M, int N, int K, const void *A, int lda, c
     a.act = act;
     a.ztype = ztype;
     a.direct = whole(A, lda, true, M) && whole(G, ldg, true, N) && whole(U, ldu, true, N);
+    a.near = lda < 1 << 23 && ldg < 1 << 23 && ldu < 1 << 23 && K >= 8;
     return launch(type, true, false, true, a, stream);
 }

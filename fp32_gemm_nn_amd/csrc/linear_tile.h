@@ -25,6 +25,13 @@ __device__ __forceinline__ void meet() {
     __builtin_amdgcn_s_barrier();
     asm volatile("" ::: "memory");
 }
+// The same with loads to registers left on their way.
+__device__ __forceinline__ void meet_lds() {
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_waitcnt(0xC07F);   // LDS's counter alone
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+}
 // The same with each wave's last N loads to LDS left on their way.
 template <int N> __device__ __forceinline__ void meet_but() {
     static_assert(N >= 0 && N < 64, "the counter's range");
@@ -112,7 +119,9 @@ template <class T> struct Chunk {
     }
 };
 
-enum Way { DIRECT, STAGED };   // operands to LDS: without registers, or through them at any alignment
+// Operands to LDS: without registers; through them at any alignment, for leading
+// dimensions below 2^23 and rows of eight values at least; the same for any.
+enum Way { DIRECT, STAGED, FAR };
 
 // BUFS blocks of k have room in LDS: one that is read, the others on their way.
 template <class T, int BM, int BN, int WM, int WN, int BUFS, bool KA, bool KB, bool GATED, Way WAY>
@@ -164,6 +173,22 @@ __global__ __launch_bounds__(64 * WM * WN, WM * WN / 4 * (2 * BUFS * (BM + BN) *
                            : r * ld * 2 + 16 * min(c, (g.N - n0) / 8 - 1);
         }
     }
+    if constexpr (WAY == STAGED) {
+        // Offsets of whole rows of a block of k, 16 bytes high to keep them
+        // positive; across k (or, where k is across, along the outputs) they go
+        // back to the row's last 16 bytes where it ends.
+#pragma unroll
+        for (int j = 0; j < PanelA::PER; ++j) {
+            const int r = PanelA::row(tid, j), c = 16 * PanelA::chunk(tid, j);
+            from_a[j] = (KA ? min(r, g.M - 1 - m0) : r) * (uint32_t)g.lda * 2 + 16 + (KA ? 0 : min(c, 2 * (g.M - m0) - 16));
+        }
+#pragma unroll
+        for (int j = 0; j < PanelB::PER; ++j) {
+            const int r = PanelB::row(tid, j), c = 16 * PanelB::chunk(tid, j);
+            from_b[j] = (KB ? min(column(r), g.N - 1 - n0) : r) * (uint32_t)(second(r) ? g.ldu : g.ldb) * 2 + 16 +
+                        (KB ? 0 : min(c, 2 * (g.N - n0) - 16));
+        }
+    }
     auto copy_a = [&](int kb, int buf, int j) {
         const T *src = KA ? A + m0 * g.lda + (long long)kb * kStep : A + (long long)kb * kStep * g.lda + m0;
         load_lds(src, from_a[j], lds + buf * BYTES + 1024 * wave + 16 * NT * j);
@@ -188,7 +213,41 @@ __global__ __launch_bounds__(64 * WM * WN, WM * WN / 4 * (2 * BUFS * (BM + BN) *
     struct Chunks {
         Chunk<T> a[PanelA::PER], b[PanelB::PER];
     };
+    // A block's 16 bytes of each of a thread's chunks, by offsets from its beginning.
+    auto fetch_near = [&](Chunks &w, int kb) {
+        asm("" : "+s"(kb));   // hides that kb counts a loop: each load would get a pointer of its own
+        const int left = g.K - kb * kStep;
+        auto get = [](const T *base, uint32_t offset) {
+            return *reinterpret_cast<const typename Chunk<T>::words *>(reinterpret_cast<const uint8_t *>(base) - 16 + offset);
+        };
+        // Rows of k past its end: the last one's, to be cleared.
+        auto across = [&](uint32_t from, int r, long long ld) {
+            return left >= kStep ? from : from - max(r - (left - 1), 0) * (uint32_t)ld * 2;
+        };
+#pragma unroll
+        for (int j = 0; j < PanelA::PER; ++j) {
+            const int c = 16 * PanelA::chunk(tid, j);
+            if (KA)
+                w.a[j].w = get(A + m0 * g.lda + (long long)kb * kStep, from_a[j] + min(c, 2 * left - 16));
+            else
+                w.a[j].w = get(A + (long long)kb * kStep * g.lda + m0, across(from_a[j], PanelA::row(tid, j), g.lda));
+        }
+#pragma unroll
+        for (int j = 0; j < PanelB::PER; ++j) {
+            const int c = 16 * PanelB::chunk(tid, j);
+            if (KB) {
+                const bool u = second(8 * wave + NT / 8 * j);   // eight rows of a wave are of one weight
+                w.b[j].w = get((u ? U + n0 * g.ldu : B + n0 * g.ldb) + (long long)kb * kStep, from_b[j] + min(c, 2 * left - 16));
+            } else {
+                w.b[j].w = get(B + (long long)kb * kStep * g.ldb + n0, across(from_b[j], PanelB::row(tid, j), g.ldb));
+            }
+        }
+    };
     auto fetch = [&](Chunks &w, int kb) {
+        if constexpr (WAY == STAGED) {
+            fetch_near(w, kb);
+            return;
+        }
         const int k0 = kb * kStep;
 #pragma unroll
         for (int j = 0; j < PanelA::PER; ++j) {
@@ -273,18 +332,39 @@ __global__ __launch_bounds__(64 * WM * WN, WM * WN / 4 * (2 * BUFS * (BM + BN) *
     };
     auto nothing = [](int) {};
 
-    const int last = WAY == STAGED ? kb1 : min(kb1, g.K / kStep);   // the blocks that the loop takes
+    const int last = WAY != DIRECT ? kb1 : min(kb1, g.K / kStep);   // the blocks that the loop takes
     if (kb0 < last) {
         constexpr int PER = PanelA::PER + PanelB::PER, AHEAD = BUFS - 1;
-        Chunks w;
-        if constexpr (WAY == STAGED) {
-            static_assert(BUFS == 2, "the third block on its way is in registers");
-            fetch(w, kb0);
-            write(w, kb0, 0);
-            if (kb0 + 1 < last) fetch(w, kb0 + 1);
-            meet();
-            if (kb0 + 1 < last) write(w, kb0 + 1, 1);
-            if (kb0 + 2 < last) fetch(w, kb0 + 2);
+        if constexpr (WAY != DIRECT) {
+            // Two blocks in LDS, and the next ones on their way to registers:
+            // two (8% faster than one, 4096 x 4096 x 4096 with 128 x 128 outputs),
+            // but one where two workgroups to a CU have no registers for more.
+            static_assert(BUFS == 2, "");
+            constexpr int SETS = 2 * LDS <= 160 * 1024 && BM * BN >= 128 * 128 ? 1 : 2;
+            Chunks w[SETS];
+            fetch(w[0], kb0);
+            if (SETS == 2 && kb0 + 1 < last) fetch(w[SETS - 1], kb0 + 1);
+            write(w[0], kb0, 0);
+            if (kb0 + SETS < last) fetch(w[0], kb0 + SETS);
+            meet_lds();
+            if (kb0 + 1 < last) write(w[SETS - 1], kb0 + 1, 1);
+            if (kb0 + 1 + SETS < last) fetch(w[SETS - 1], kb0 + 1 + SETS);
+#pragma unroll
+            for (int p = 0; p < READS; ++p) read(0, 0, p);
+            auto block = [&](int kb, auto buf_) {
+                constexpr int buf = decltype(buf_)::value;
+                multiply(0, buf, nothing);
+                // All of this block is in registers, and the next one is written.
+                meet_lds();
+                if (kb + 2 < last) write(w[buf % SETS], kb + 2, buf);
+                if (kb + 2 + SETS < last) fetch(w[buf % SETS], kb + 2 + SETS);
+                multiply(1, buf ^ 1, nothing);
+            };
+#pragma unroll 1
+            for (int kb = kb0; kb < last; kb += 2) {
+                block(kb, std::integral_constant<int, 0>{});
+                if (kb + 1 < last) block(kb + 1, std::integral_constant<int, 1>{});
+            }
         } else {
 #pragma unroll
             for (int k = 0; k < AHEAD; ++k)
@@ -294,21 +374,14 @@ __global__ __launch_bounds__(64 * WM * WN, WM * WN / 4 * (2 * BUFS * (BM + BN) *
             else
                 meet();
             if (kb0 + AHEAD < last) copy(kb0 + AHEAD, AHEAD);
-        }
 #pragma unroll
-        for (int p = 0; p < READS; ++p) read(0, 0, p);
-        int buf = 0;
+            for (int p = 0; p < READS; ++p) read(0, 0, p);
+            int buf = 0;
 #pragma unroll 1
-        for (int kb = kb0; kb < last; ++kb) {
-            const int next = buf + 1 == BUFS ? 0 : buf + 1;
-            multiply(0, buf, nothing);
-            // All of this block is in registers, and the next one has landed.
-            if constexpr (WAY == STAGED) {
-                meet();
-                if (kb + 2 < last) write(w, kb + 2, buf);
-                if (kb + 3 < last) fetch(w, kb + 3);
-                multiply(1, next, nothing);
-            } else {
+            for (int kb = kb0; kb < last; ++kb) {
+                const int next = buf + 1 == BUFS ? 0 : buf + 1;
+                multiply(0, buf, nothing);
+                // All of this block is in registers, and the next one has landed.
                 if (BUFS > 2 && kb + BUFS <= last)
                     meet_but<PER *(BUFS - 2)>();
                 else
@@ -325,8 +398,8 @@ __global__ __launch_bounds__(64 * WM * WN, WM * WN / 4 * (2 * BUFS * (BM + BN) *
                             copy_b(kb + BUFS, buf, j - PanelA::PER);
                     }
                 });
+                buf = next;
             }
-            buf = next;
         }
     }
     if constexpr (WAY == DIRECT) {
@@ -511,13 +584,16 @@ int launch_tile(LinArgs &g, hipStream_t stream) {
 
 template <class T, bool KA, bool KB> int launch_linear(int shape, LinArgs &g, hipStream_t stream) {
     switch (shape) {
-        case 0: return launch_tile<T, 128, 128, 4, 2, 2, KA, KB, false, STAGED>(g, stream);
+        case 0:
+            if (!g.near) return launch_tile<T, 128, 128, 4, 2, 2, KA, KB, false, FAR>(g, stream);
+            return launch_tile<T, 128, 128, 4, 2, 2, KA, KB, false, STAGED>(g, stream);
         case 1: return launch_tile<T, 64, 128, 4, 2, 2, KA, KB, false, STAGED>(g, stream);
-        case 2: return launch_tile<T, 64, 128, 4, 2, 3, KA, KB, false, DIRECT>(g, stream);
-        case 3: return launch_tile<T, 128, 128, 4, 2, 2, KA, KB, false, DIRECT>(g, stream);
-        case 4: return launch_tile<T, 128, 128, 4, 2, 4, KA, KB, false, DIRECT>(g, stream);
-        case 5: return launch_tile<T, 128, 256, 2, 4, 3, KA, KB, false, DIRECT>(g, stream);
-        case 6:
+        case 2: return launch_tile<T, 256, 128, 4, 2, 2, KA, KB, false, STAGED>(g, stream);
+        case 8: return launch_tile<T, 64, 128, 4, 2, 3, KA, KB, false, DIRECT>(g, stream);
+        case 9: return launch_tile<T, 128, 128, 4, 2, 2, KA, KB, false, DIRECT>(g, stream);
+        case 10: return launch_tile<T, 128, 128, 4, 2, 4, KA, KB, false, DIRECT>(g, stream);
+        case 11: return launch_tile<T, 128, 256, 2, 4, 3, KA, KB, false, DIRECT>(g, stream);
+        case 12:
             // Waves of 64 x 128 outputs, but of 128 x 64 where B alone comes by transposing reads.
             if constexpr (KA && !KB) return launch_tile<T, 256, 256, 2, 4, 2, KA, KB, false, DIRECT>(g, stream);
             return launch_tile<T, 256, 256, 4, 2, 2, KA, KB, false, DIRECT>(g, stream);
@@ -526,14 +602,16 @@ template <class T, bool KA, bool KB> int launch_linear(int shape, LinArgs &g, hi
 }
 template <class T> int launch_gated(int shape, LinArgs &g, hipStream_t stream) {
     switch (shape) {
-        case 0: return launch_tile<T, 128, 256, 2, 4, 2, true, true, true, STAGED>(g, stream);
+        case 0:
+            if (!g.near) return launch_tile<T, 128, 256, 2, 4, 2, true, true, true, FAR>(g, stream);
+            return launch_tile<T, 128, 256, 2, 4, 2, true, true, true, STAGED>(g, stream);
         case 1: return launch_tile<T, 64, 256, 2, 4, 2, true, true, true, STAGED>(g, stream);
-        case 2: return launch_tile<T, 64, 256, 2, 4, 3, true, true, true, DIRECT>(g, stream);
-        case 3: return launch_tile<T, 64, 256, 2, 4, 2, true, true, true, DIRECT>(g, stream);
-        case 4: return launch_tile<T, 128, 128, 4, 2, 4, true, true, true, DIRECT>(g, stream);
-        case 5: return launch_tile<T, 128, 256, 2, 4, 3, true, true, true, DIRECT>(g, stream);
-        case 7: return launch_tile<T, 128, 128, 4, 2, 2, true, true, true, DIRECT>(g, stream);
-        case 6: return launch_tile<T, 256, 256, 4, 2, 2, true, true, true, DIRECT>(g, stream);
+        case 8: return launch_tile<T, 64, 256, 2, 4, 3, true, true, true, DIRECT>(g, stream);
+        case 9: return launch_tile<T, 64, 256, 2, 4, 2, true, true, true, DIRECT>(g, stream);
+        case 10: return launch_tile<T, 128, 128, 4, 2, 4, true, true, true, DIRECT>(g, stream);
+        case 11: return launch_tile<T, 128, 128, 4, 2, 2, true, true, true, DIRECT>(g, stream);
+        case 12: return launch_tile<T, 128, 256, 2, 4, 3, true, true, true, DIRECT>(g, stream);
+        case 13: return launch_tile<T, 256, 256, 4, 2, 2, true, true, true, DIRECT>(g, stream);
         default: return MISGEMM_LAUNCH_FAILED;
     }
 }
