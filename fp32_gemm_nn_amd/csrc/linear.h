@@ -38,10 +38,10 @@ struct LinArgs {
 // steps of a result's last place are the least error there is; e^x as 2^(x / ln 2)
 // is off by |x| of them at most. Where z is infinite a factor that would make
 // NaN of the other's 0 is held at 104, beyond which f and f' are at their limits
-// (v_max_f32 and v_min_f32 drop NaN, so the other factor has to carry it).
+// (v_med3_f32 drops NaN, so the other factor has to carry it).
 constexpr float kLog2E = 1.44269504f;
-__device__ __forceinline__ float above(float z) { return fmaxf(z, -104.0f); }
-__device__ __forceinline__ float within(float z) { return fminf(fmaxf(z, -104.0f), 104.0f); }
+__device__ __forceinline__ float above(float z) { return __builtin_amdgcn_fmed3f(z, -104.0f, __builtin_inff()); }
+__device__ __forceinline__ float within(float z) { return __builtin_amdgcn_fmed3f(z, -104.0f, 104.0f); }
 
 // 1 / (1 + e^-z).
 __device__ __forceinline__ float sigmoid(float z) {
@@ -135,46 +135,64 @@ template <class T, int N> __device__ __forceinline__ void bias_at(const void *bi
     }
 }
 
-// One row's N neighbouring values from column n on: z (unless it has 8 bits),
-// then f(z) + beta R. R may be C: a value is read by the thread that writes it.
-template <class CT, int N> __device__ __forceinline__ void put_linear(const LinArgs &g, int m, int n, float (&v)[N]) {
-    const int left = g.N - n;
-    if (g.z != nullptr && g.zs == nullptr) store<CT, N>(static_cast<CT *>(g.z) + m * g.ldz + n, left, v);
-    activate<N>(g.act, v);
-    if (g.beta != 0.0f) {
-        float r[N];
-        load<CT, N>(static_cast<const CT *>(g.R) + m * g.ldr + n, left, r);
+// R rows, `step` apart from row m on, of N neighbouring values each from column
+// n on (n < N): z (unless it has 8 bits), then f(z) + beta R. R may be C: a value
+// is read by the thread that writes it. WHOLE: all of them are in the matrix.
+template <class CT, int R, int N, bool WHOLE>
+__device__ __forceinline__ void put_linear(const LinArgs &g, int m, int step, int n, float (&v)[R * N]) {
+    const int left = WHOLE ? N : g.N - n;
+    auto each = [&](void *base, long long ld, auto f) {
+        CT *p = static_cast<CT *>(base) + m * ld + n;
 #pragma unroll
-        for (int j = 0; j < N; ++j) v[j] = fmaf(g.beta, r[j], v[j]);
-    }
-    store<CT, N>(static_cast<CT *>(g.C) + m * g.ldc + n, left, v);
+        for (int r = 0; r < R; ++r)
+            if (WHOLE || m + r * step < g.M) f(p + r * (step * ld), *reinterpret_cast<float(*)[N]>(v + r * N));
+    };
+    auto write = [&](CT *p, float (&row)[N]) { store<CT, N>(p, left, row); };
+    if (g.z != nullptr && g.zs == nullptr) each(g.z, g.ldz, write);
+    activate<R * N>(g.act, v);
+    if (g.beta != 0.0f)
+        each(const_cast<void *>(g.R), g.ldr, [&](const CT *p, float (&row)[N]) {
+            float old[N];
+            load<CT, N>(p, left, old);
+#pragma unroll
+            for (int j = 0; j < N; ++j) row[j] = fmaf(g.beta, old[j], row[j]);
+        });
+    each(g.C, g.ldc, write);
 }
 // The gated block's: v is g and then h, u is u.
-template <class CT, int N>
-__device__ __forceinline__ void put_gated(const LinArgs &g, int m, int n, float (&v)[N], const float (&u)[N]) {
-    const int left = g.N - n;
-    if (g.z != nullptr && g.zs == nullptr) {
-        store<CT, N>(static_cast<CT *>(g.z) + m * g.ldz + n, left, v);
-        store<CT, N>(static_cast<CT *>(g.zu) + m * g.ldzu + n, left, u);
-    }
-    activate<N>(g.act, v);
+template <class CT, int R, int N, bool WHOLE>
+__device__ __forceinline__ void put_gated(const LinArgs &g, int m, int step, int n, float (&v)[R * N],
+                                          float (&u)[R * N]) {
+    const int left = WHOLE ? N : g.N - n;
+    auto write = [&](void *base, long long ld, float (&x)[R * N]) {
+        CT *p = static_cast<CT *>(base) + m * ld + n;
 #pragma unroll
-    for (int j = 0; j < N; ++j) v[j] *= u[j];
-    store<CT, N>(static_cast<CT *>(g.C) + m * g.ldc + n, left, v);
+        for (int r = 0; r < R; ++r)
+            if (WHOLE || m + r * step < g.M)
+                store<CT, N>(p + r * (step * ld), left, *reinterpret_cast<float(*)[N]>(x + r * N));
+    };
+    if (g.z != nullptr && g.zs == nullptr) {
+        write(g.z, g.ldz, v);
+        write(g.zu, g.ldzu, u);
+    }
+    activate<R * N>(g.act, v);
+#pragma unroll
+    for (int j = 0; j < R * N; ++j) v[j] *= u[j];
+    write(g.C, g.ldc, v);
 }
-template <class T, bool GATED, int N>
-__device__ __forceinline__ void put_out(const LinArgs &g, int m, int n, float (&v)[N], const float (&u)[N]) {
-    if (m >= g.M || n >= g.N) return;
+template <class T, bool GATED, int R, int N, bool WHOLE>
+__device__ __forceinline__ void put_out(const LinArgs &g, int m, int step, int n, float (&v)[R * N],
+                                        float (&u)[R * N]) {
     if constexpr (GATED) {
         if (g.c32)
-            put_gated<float, N>(g, m, n, v, u);
+            put_gated<float, R, N, WHOLE>(g, m, step, n, v, u);
         else
-            put_gated<T, N>(g, m, n, v, u);
+            put_gated<T, R, N, WHOLE>(g, m, step, n, v, u);
     } else {
         if (g.c32)
-            put_linear<float, N>(g, m, n, v);
+            put_linear<float, R, N, WHOLE>(g, m, step, n, v);
         else
-            put_linear<T, N>(g, m, n, v);
+            put_linear<T, R, N, WHOLE>(g, m, step, n, v);
     }
 }
 

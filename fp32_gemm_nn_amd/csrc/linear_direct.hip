@@ -153,7 +153,7 @@ __global__ __launch_bounds__(64 * W) void lin_direct(LinArgs g) {
     __syncthreads();
     auto total = [&](int f, float (&v)[4], const void *bias, int n) {
         f32x4 sum = reinterpret_cast<const f32x4 *>(lds[0])[64 * f + lane];
-#pragma unroll
+#pragma unroll 5
         for (int w = 1; w < W; ++w) sum += reinterpret_cast<const f32x4 *>(lds[w])[64 * f + lane];
         float more[4];
         bias_at<T, 4>(bias, g.bias32, n, g.N - n, more);
@@ -168,7 +168,8 @@ __global__ __launch_bounds__(64 * W) void lin_direct(LinArgs g) {
         float v[4], u[4] = {};
         total(a * NB + b, v, g.bias, col);
         if constexpr (GATED) total(a * NB + NH + b, u, g.bias_u, col);
-        put_out<T, GATED, 4>(g, m0 + 16 * a + i, col, v, u);
+        const int m = m0 + 16 * a + i;
+        if (m < g.M && col < g.N) put_out<T, GATED, 1, 4, false>(g, m, 0, col, v, u);
     }
 }
 
@@ -184,7 +185,7 @@ template <class T, int MB, int NB, int W, int D, bool GATED> int launch_shape(Li
 template <class T> int launch(bool gated, int shape, LinArgs &g, hipStream_t stream) {
     if (gated) {
         switch (shape) {
-            case 0: return launch_shape<T, 1, 2, 16, 2, true>(g, stream);
+            case 0: return launch_shape<T, 1, 2, 16, 1, true>(g, stream);
             case 1: return launch_shape<T, 1, 2, 8, 2, true>(g, stream);
             case 2: return launch_shape<T, 1, 4, 8, 2, true>(g, stream);
             case 3: return launch_shape<T, 2, 2, 8, 2, true>(g, stream);

@@ -316,7 +316,7 @@ __global__ __launch_bounds__(64 * WM * WN, WM * WN / 4 * (2 * BUFS * (BM + BN) *
     // all rows, others over three quarters of them (each the faster, by 1 to 3%).
     // Every other row goes backwards: one operand stays from product to product.
     auto upto = [](int a) { return min(READS, KA && KB ? READS * a * 4 / (3 * MI) : READS * a / MI); };
-    auto multiply = [&](int s, int next_buf, auto more) {
+    auto multiply = [&](int s, int next_buf, auto more) __attribute__((always_inline)) {
 #pragma unroll
         for (int a = 0; a < MI; ++a) {
 #pragma unroll
@@ -457,6 +457,7 @@ __global__ __launch_bounds__(64 * WM * WN, WM * WN / 4 * (2 * BUFS * (BM + BN) *
     meet();
     const int m1 = m0 + wm * TM, n1 = n0 + wn * (GATED ? TN / 2 : TN);
     constexpr int NH = GATED ? NI / 2 : NI;   // sixteens of columns of outputs
+    if (g.alpha != 1.0f || g.bias != nullptr || (GATED && g.bias_u != nullptr))
 #pragma unroll
     for (int b = 0; b < NI; ++b) {
         const int n = n1 + 16 * (b % NH) + 4 * grp;
@@ -512,56 +513,76 @@ __global__ __launch_bounds__(64 * WM * WN, WM * WN / 4 * (2 * BUFS * (BM + BN) *
     }
     // Outputs turn in LDS, each wave's in its own, and leave as whole rows:
     // 64 columns at a time, or 32 and 32 of the two projections. Chunk c (four
-    // values) of row r is at c ^ (r & 15).
+    // values) of row r is at c ^ (r & 15). A lane takes eight columns of up to
+    // four rows at once, so that their reads and the choices on the way (the
+    // activation, types, what is kept) are shared; where the tile ends inside
+    // the matrix, without a bound to check.
     f32x4 *own = reinterpret_cast<f32x4 *>(lds) + wave * ROWS * 256;
-    constexpr int LANES = GATED ? 4 : 8;   // of a row
+    constexpr int LANES = GATED ? 4 : 8, STEP = 64 / LANES;   // of a row; rows at a time
+    constexpr int SETS = 16 * ROWS / STEP, R = SETS < 4 ? SETS : 4;
+    auto leave = [&](auto whole_) __attribute__((always_inline)) {
+        constexpr bool WHOLE = decltype(whole_)::value;
 #pragma unroll
-    for (int p = 0; p < NI / 4; ++p)
+        for (int p = 0; p < NI / 4; ++p)
 #pragma unroll
-        for (int a0 = 0; a0 < MI; a0 += ROWS) {
+            for (int a0 = 0; a0 < MI; a0 += ROWS) {
 #pragma unroll
-            for (int a = 0; a < ROWS; ++a)
+                for (int a = 0; a < ROWS; ++a)
 #pragma unroll
-                for (int b = 0; b < 4; ++b)
-                    own[(16 * a + i) * 16 + ((4 * b + grp) ^ i)] =
-                        acc[a0 + a][GATED ? (b < 2 ? 2 * p + b : NH + 2 * p + b - 2) : 4 * p + b];
-            asm volatile("" ::: "memory");
+                    for (int b = 0; b < 4; ++b)
+                        own[(16 * a + i) * 16 + ((4 * b + grp) ^ i)] =
+                            acc[a0 + a][GATED ? (b < 2 ? 2 * p + b : NH + 2 * p + b - 2) : 4 * p + b];
+                asm volatile("" ::: "memory");
 #pragma unroll 1
-            for (int r0 = 0; r0 < 16 * ROWS; r0 += 64 / LANES) {
-                const int r = r0 + lane / LANES, c = lane % LANES * 2;
-                const int m = m1 + 16 * a0 + r, n = n1 + (GATED ? 32 : 64) * p + 4 * c;
-                float v[8], u[8];
+                for (int s0 = 0; s0 < SETS; s0 += R) {
+                    const int r0 = s0 * STEP + lane / LANES, c = lane % LANES * 2;
+                    const int m = m1 + 16 * a0 + r0, n = n1 + (GATED ? 32 : 64) * p + 4 * c;
+                    float v[8 * R], u[8 * R];
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const f32x4 x = own[r * 16 + ((c + h) ^ (r & 15))];
-                    f32x4 y = {};
-                    if constexpr (GATED) y = own[r * 16 + ((8 + c + h) ^ (r & 15))];
+                    for (int s = 0; s < R; ++s)
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        v[4 * h + j] = x[j];
-                        u[4 * h + j] = y[j];
-                    }
-                }
-                if (in8 && m < g.M && n < g.N) {
-                    auto keep = [&](const float (&z)[8], int part, void *q, long long ldq) {
-                        const float f = maxes[part * SHARE * BM + wm * TM + 16 * a0 + r];
-                        int w[2];
-                        if (g.ztype == MI_E4M3) {
-                            w[0] = pack4<MI_E4M3>(z[0] * f, z[1] * f, z[2] * f, z[3] * f);
-                            w[1] = pack4<MI_E4M3>(z[4] * f, z[5] * f, z[6] * f, z[7] * f);
-                        } else {
-                            w[0] = pack4<MI_E5M2>(z[0] * f, z[1] * f, z[2] * f, z[3] * f);
-                            w[1] = pack4<MI_E5M2>(z[4] * f, z[5] * f, z[6] * f, z[7] * f);
+                        for (int h = 0; h < 2; ++h) {
+                            const int r = r0 + s * STEP;
+                            const f32x4 x = own[r * 16 + ((c + h) ^ (r & 15))];
+                            f32x4 y = {};
+                            if constexpr (GATED) y = own[r * 16 + ((8 + c + h) ^ (r & 15))];
+#pragma unroll
+                            for (int j = 0; j < 4; ++j) {
+                                v[8 * s + 4 * h + j] = x[j];
+                                u[8 * s + 4 * h + j] = y[j];
+                            }
                         }
-                        store_bytes<8>(static_cast<uint8_t *>(q) + m * ldq + n, g.N - n, w);
-                    };
-                    keep(v, GATED ? 0 : wn / SHARE, g.z, g.ldz);
-                    if constexpr (GATED) keep(u, 1, g.zu, g.ldzu);
+                    if (!WHOLE && n >= g.N) continue;
+                    if (in8) {
+                        auto keep = [&](const float *z, int part, void *q, long long ldq) {
+                            uint8_t *to = static_cast<uint8_t *>(q) + m * ldq + n;
+#pragma unroll
+                            for (int s = 0; s < R; ++s, z += 8) {
+                                const float f = maxes[part * SHARE * BM + wm * TM + 16 * a0 + r0 + s * STEP];
+                                int w[2];
+                                if (g.ztype == MI_E4M3) {
+                                    w[0] = pack4<MI_E4M3>(z[0] * f, z[1] * f, z[2] * f, z[3] * f);
+                                    w[1] = pack4<MI_E4M3>(z[4] * f, z[5] * f, z[6] * f, z[7] * f);
+                                } else {
+                                    w[0] = pack4<MI_E5M2>(z[0] * f, z[1] * f, z[2] * f, z[3] * f);
+                                    w[1] = pack4<MI_E5M2>(z[4] * f, z[5] * f, z[6] * f, z[7] * f);
+                                }
+                                if (WHOLE || m + s * STEP < g.M)
+                                    store_bytes<8>(to + s * (STEP * ldq), WHOLE ? 8 : g.N - n, w);
+                            }
+                        };
+                        keep(v, GATED ? 0 : wn / SHARE, g.z, g.ldz);
+                        if constexpr (GATED) keep(u, 1, g.zu, g.ldzu);
+                    }
+                    put_out<T, GATED, R, 8, WHOLE>(g, m, STEP, n, v, u);
                 }
-                put_out<T, GATED, 8>(g, m, n, v, u);
+                asm volatile("" ::: "memory");
             }
-            asm volatile("" ::: "memory");
-        }
+    };
+    if (m0 + BM <= g.M && n0 + COLS <= g.N)
+        leave(std::true_type{});
+    else
+        leave(std::false_type{});
 }
 
 template <class T, int BM, int BN, int WM, int WN, int BUFS, bool KA, bool KB, bool GATED, Way WAY>
