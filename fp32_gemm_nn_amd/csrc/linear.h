@@ -135,10 +135,33 @@ template <class T, int N> __device__ __forceinline__ void bias_at(const void *bi
     }
 }
 
+// N values or bytes to memory, past L2 where they STREAM: a large product's
+// outputs would push out operands that neighbours read (8192 x 8192 x 4096 with
+// an 8-bit checkpoint 400 us, 417 through L2; gated 744 and 761).
+template <class CT, int N, bool STREAM> __device__ __forceinline__ void put(CT *p, int left, const float (&v)[N]) {
+    // FP32 leaves in half lines, which L2 has to join (196 us and 205 past it, 4096 x 4096 x 8192).
+    if (STREAM && sizeof(CT) == 2 && left >= N) {
+        typedef typename Values<CT, N>::type type;
+        type w;
+#pragma unroll
+        for (int j = 0; j < N; ++j) w[j] = static_cast<CT>(v[j]);
+        __builtin_nontemporal_store(w, reinterpret_cast<type *>(p));
+    } else {
+        store<CT, N>(p, left, v);
+    }
+}
+template <bool STREAM> __device__ __forceinline__ void put_bytes(uint8_t *p, int left, const int (&w)[2]) {
+    typedef int words __attribute__((ext_vector_type(2), aligned(1)));
+    if (STREAM && left >= 8)
+        __builtin_nontemporal_store(words{w[0], w[1]}, reinterpret_cast<words *>(p));
+    else
+        store_bytes<8>(p, left, w);
+}
+
 // R rows, `step` apart from row m on, of N neighbouring values each from column
 // n on (n < N): z (unless it has 8 bits), then f(z) + beta R. R may be C: a value
 // is read by the thread that writes it. WHOLE: all of them are in the matrix.
-template <class CT, int R, int N, bool WHOLE>
+template <class CT, int R, int N, bool WHOLE, bool STREAM>
 __device__ __forceinline__ void put_linear(const LinArgs &g, int m, int step, int n, float (&v)[R * N]) {
     const int left = WHOLE ? N : g.N - n;
     auto each = [&](void *base, long long ld, auto f) {
@@ -147,7 +170,7 @@ __device__ __forceinline__ void put_linear(const LinArgs &g, int m, int step, in
         for (int r = 0; r < R; ++r)
             if (WHOLE || m + r * step < g.M) f(p + r * (step * ld), *reinterpret_cast<float(*)[N]>(v + r * N));
     };
-    auto write = [&](CT *p, float (&row)[N]) { store<CT, N>(p, left, row); };
+    auto write = [&](CT *p, float (&row)[N]) { put<CT, N, STREAM>(p, left, row); };
     if (g.z != nullptr && g.zs == nullptr) each(g.z, g.ldz, write);
     activate<R * N>(g.act, v);
     if (g.beta != 0.0f)
@@ -160,7 +183,7 @@ __device__ __forceinline__ void put_linear(const LinArgs &g, int m, int step, in
     each(g.C, g.ldc, write);
 }
 // The gated block's: v is g and then h, u is u.
-template <class CT, int R, int N, bool WHOLE>
+template <class CT, int R, int N, bool WHOLE, bool STREAM>
 __device__ __forceinline__ void put_gated(const LinArgs &g, int m, int step, int n, float (&v)[R * N],
                                           float (&u)[R * N]) {
     const int left = WHOLE ? N : g.N - n;
@@ -169,7 +192,7 @@ __device__ __forceinline__ void put_gated(const LinArgs &g, int m, int step, int
 #pragma unroll
         for (int r = 0; r < R; ++r)
             if (WHOLE || m + r * step < g.M)
-                store<CT, N>(p + r * (step * ld), left, *reinterpret_cast<float(*)[N]>(x + r * N));
+                put<CT, N, STREAM>(p + r * (step * ld), left, *reinterpret_cast<float(*)[N]>(x + r * N));
     };
     if (g.z != nullptr && g.zs == nullptr) {
         write(g.z, g.ldz, v);
@@ -180,19 +203,19 @@ __device__ __forceinline__ void put_gated(const LinArgs &g, int m, int step, int
     for (int j = 0; j < R * N; ++j) v[j] *= u[j];
     write(g.C, g.ldc, v);
 }
-template <class T, bool GATED, int R, int N, bool WHOLE>
+template <class T, bool GATED, int R, int N, bool WHOLE, bool STREAM>
 __device__ __forceinline__ void put_out(const LinArgs &g, int m, int step, int n, float (&v)[R * N],
                                         float (&u)[R * N]) {
     if constexpr (GATED) {
         if (g.c32)
-            put_gated<float, R, N, WHOLE>(g, m, step, n, v, u);
+            put_gated<float, R, N, WHOLE, STREAM>(g, m, step, n, v, u);
         else
-            put_gated<T, R, N, WHOLE>(g, m, step, n, v, u);
+            put_gated<T, R, N, WHOLE, STREAM>(g, m, step, n, v, u);
     } else {
         if (g.c32)
-            put_linear<float, R, N, WHOLE>(g, m, step, n, v);
+            put_linear<float, R, N, WHOLE, STREAM>(g, m, step, n, v);
         else
-            put_linear<T, R, N, WHOLE>(g, m, step, n, v);
+            put_linear<T, R, N, WHOLE, STREAM>(g, m, step, n, v);
     }
 }
 

@@ -520,6 +520,7 @@ __global__ __launch_bounds__(64 * WM * WN, WM * WN / 4 * (2 * BUFS * (BM + BN) *
     f32x4 *own = reinterpret_cast<f32x4 *>(lds) + wave * ROWS * 256;
     constexpr int LANES = GATED ? 4 : 8, STEP = 64 / LANES;   // of a row; rows at a time
     constexpr int SETS = 16 * ROWS / STEP, R = SETS < 4 ? SETS : 4;
+    constexpr bool STREAM = BM * BN == 256 * 256;
     auto leave = [&](auto whole_) __attribute__((always_inline)) {
         constexpr bool WHOLE = decltype(whole_)::value;
 #pragma unroll
@@ -568,13 +569,13 @@ __global__ __launch_bounds__(64 * WM * WN, WM * WN / 4 * (2 * BUFS * (BM + BN) *
                                     w[1] = pack4<MI_E5M2>(z[4] * f, z[5] * f, z[6] * f, z[7] * f);
                                 }
                                 if (WHOLE || m + s * STEP < g.M)
-                                    store_bytes<8>(to + s * (STEP * ldq), WHOLE ? 8 : g.N - n, w);
+                                    put_bytes<STREAM>(to + s * (STEP * ldq), WHOLE ? 8 : g.N - n, w);
                             }
                         };
                         keep(v, GATED ? 0 : wn / SHARE, g.z, g.ldz);
                         if constexpr (GATED) keep(u, 1, g.zu, g.ldzu);
                     }
-                    put_out<T, GATED, R, 8, WHOLE>(g, m, STEP, n, v, u);
+                    put_out<T, GATED, R, 8, WHOLE, STREAM>(g, m, STEP, n, v, u);
                 }
                 asm volatile("" ::: "memory");
             }
@@ -616,8 +617,10 @@ template <class T, bool KA, bool KB> int launch_linear(int shape, LinArgs &g, hi
         case 11: return launch_tile<T, 128, 256, 2, 4, 3, KA, KB, false, DIRECT>(g, stream);
         case 12:
             // Waves of 64 x 128 outputs, but of 128 x 64 where B alone comes by transposing reads.
-            if constexpr (KA && !KB) return launch_tile<T, 256, 256, 2, 4, 2, KA, KB, false, DIRECT>(g, stream);
-            return launch_tile<T, 256, 256, 4, 2, 2, KA, KB, false, DIRECT>(g, stream);
+            if constexpr (KA && !KB)
+                return launch_tile<T, 256, 256, 2, 4, 2, KA, KB, false, DIRECT>(g, stream);
+            else
+                return launch_tile<T, 256, 256, 4, 2, 2, KA, KB, false, DIRECT>(g, stream);
         default: return MISGEMM_LAUNCH_FAILED;
     }
 }
