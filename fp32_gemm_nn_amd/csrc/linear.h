@@ -139,8 +139,7 @@ template <class T, int N> __device__ __forceinline__ void bias_at(const void *bi
 // outputs would push out operands that neighbours read (8192 x 8192 x 4096 with
 // an 8-bit checkpoint 400 us, 417 through L2; gated 744 and 761).
 template <class CT, int N, bool STREAM> __device__ __forceinline__ void put(CT *p, int left, const float (&v)[N]) {
-    // FP32 leaves in half lines, which L2 has to join (196 us and 205 past it, 4096 x 4096 x 8192).
-    if (STREAM && sizeof(CT) == 2 && left >= N) {
+    if (STREAM && left >= N) {
         typedef typename Values<CT, N>::type type;
         type w;
 #pragma unroll
@@ -150,35 +149,48 @@ template <class CT, int N, bool STREAM> __device__ __forceinline__ void put(CT *
         store<CT, N>(p, left, v);
     }
 }
-template <bool STREAM> __device__ __forceinline__ void put_bytes(uint8_t *p, int left, const int (&w)[2]) {
+// `apart`: the second four bytes go 32 columns on.
+template <bool STREAM> __device__ __forceinline__ void put_bytes(uint8_t *p, int left, const int (&w)[2], bool apart) {
     typedef int words __attribute__((ext_vector_type(2), aligned(1)));
+    if (apart) {
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+            if (k % 4 + 32 * (k / 4) < left)
+                p[k % 4 + 32 * (k / 4)] = static_cast<uint8_t>(static_cast<unsigned>(w[k / 4]) >> (8 * (k % 4)));
+        return;
+    }
     if (STREAM && left >= 8)
         __builtin_nontemporal_store(words{w[0], w[1]}, reinterpret_cast<words *>(p));
     else
         store_bytes<8>(p, left, w);
 }
 
-// R rows, `step` apart from row m on, of N neighbouring values each from column
-// n on (n < N): z (unless it has 8 bits), then f(z) + beta R. R may be C: a value
-// is read by the thread that writes it. WHOLE: all of them are in the matrix.
-template <class CT, int R, int N, bool WHOLE, bool STREAM>
-__device__ __forceinline__ void put_linear(const LinArgs &g, int m, int step, int n, float (&v)[R * N]) {
-    const int left = WHOLE ? N : g.N - n;
+// R rows, `step` apart from row m on, of PER pieces of N neighbouring values
+// each, 32 columns apart from column n on (n < N): z (unless it has 8 bits), then
+// f(z) + beta R. R may be C: a value is read by the thread that writes it. WHOLE:
+// all of them are in the matrix.
+template <class CT, int R, int PER, int N, bool WHOLE, bool STREAM>
+__device__ __forceinline__ void put_linear(const LinArgs &g, int m, int step, int n, float (&v)[R * PER * N]) {
     auto each = [&](void *base, long long ld, auto f) {
         CT *p = static_cast<CT *>(base) + m * ld + n;
 #pragma unroll
         for (int r = 0; r < R; ++r)
-            if (WHOLE || m + r * step < g.M) f(p + r * (step * ld), *reinterpret_cast<float(*)[N]>(v + r * N));
+#pragma unroll
+            for (int k = 0; k < PER; ++k) {
+                const int left = WHOLE ? N : g.N - n - 32 * k;
+                if (WHOLE || (m + r * step < g.M && left > 0))
+                    f(p + r * (step * ld) + 32 * k, left, *reinterpret_cast<float(*)[N]>(v + (r * PER + k) * N));
+            }
     };
-    auto write = [&](CT *p, float (&row)[N]) { put<CT, N, STREAM>(p, left, row); };
+    auto write = [&](CT *p, int left, float (&x)[N]) { put<CT, N, STREAM>(p, left, x); };
     if (g.z != nullptr && g.zs == nullptr) each(g.z, g.ldz, write);
-    activate<R * N>(g.act, v);
+    activate<R * PER * N>(g.act, v);
     if (g.beta != 0.0f)
-        each(const_cast<void *>(g.R), g.ldr, [&](const CT *p, float (&row)[N]) {
+        each(const_cast<void *>(g.R), g.ldr, [&](const CT *p, int left, float (&x)[N]) {
             float old[N];
             load<CT, N>(p, left, old);
 #pragma unroll
-            for (int j = 0; j < N; ++j) row[j] = fmaf(g.beta, old[j], row[j]);
+            for (int j = 0; j < N; ++j) x[j] = fmaf(g.beta, old[j], x[j]);
         });
     each(g.C, g.ldc, write);
 }
@@ -203,7 +215,8 @@ __device__ __forceinline__ void put_gated(const LinArgs &g, int m, int step, int
     for (int j = 0; j < R * N; ++j) v[j] *= u[j];
     write(g.C, g.ldc, v);
 }
-template <class T, bool GATED, int R, int N, bool WHOLE, bool STREAM>
+// PIECES: of FP32 (and not gated) each eight values are two pieces of four.
+template <class T, bool GATED, int R, int N, bool WHOLE, bool STREAM, bool PIECES>
 __device__ __forceinline__ void put_out(const LinArgs &g, int m, int step, int n, float (&v)[R * N],
                                         float (&u)[R * N]) {
     if constexpr (GATED) {
@@ -212,10 +225,11 @@ __device__ __forceinline__ void put_out(const LinArgs &g, int m, int step, int n
         else
             put_gated<T, R, N, WHOLE, STREAM>(g, m, step, n, v, u);
     } else {
+        constexpr int PER = PIECES ? 2 : 1;
         if (g.c32)
-            put_linear<float, R, N, WHOLE, STREAM>(g, m, step, n, v);
+            put_linear<float, R, PER, N / PER, WHOLE, STREAM>(g, m, step, n, v);
         else
-            put_linear<T, R, N, WHOLE, STREAM>(g, m, step, n, v);
+            put_linear<T, R, 1, N, WHOLE, STREAM>(g, m, step, n, v);
     }
 }
 

@@ -169,7 +169,7 @@ __global__ __launch_bounds__(64 * W) void lin_direct(LinArgs g) {
         total(a * NB + b, v, g.bias, col);
         if constexpr (GATED) total(a * NB + NH + b, u, g.bias_u, col);
         const int m = m0 + 16 * a + i;
-        if (m < g.M && col < g.N) put_out<T, GATED, 1, 4, false, false>(g, m, 0, col, v, u);
+        if (m < g.M && col < g.N) put_out<T, GATED, 1, 4, false, false, false>(g, m, 0, col, v, u);
     }
 }
 

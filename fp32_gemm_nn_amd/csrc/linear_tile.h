@@ -536,7 +536,9 @@ __global__ __launch_bounds__(64 * WM * WN, WM * WN / 4 * (2 * BUFS * (BM + BN) *
                 asm volatile("" ::: "memory");
 #pragma unroll 1
                 for (int s0 = 0; s0 < SETS; s0 += R) {
-                    const int r0 = s0 * STEP + lane / LANES, c = lane % LANES * 2;
+                    // Chunk c and the next one, or (FP32: a lane's 16 bytes beside its neighbours') the eighth from it.
+                    const bool apart = !GATED && g.c32;
+                    const int r0 = s0 * STEP + lane / LANES, c = lane % LANES * (apart ? 1 : 2);
                     const int m = m1 + 16 * a0 + r0, n = n1 + (GATED ? 32 : 64) * p + 4 * c;
                     float v[8 * R], u[8 * R];
 #pragma unroll
@@ -544,7 +546,7 @@ __global__ __launch_bounds__(64 * WM * WN, WM * WN / 4 * (2 * BUFS * (BM + BN) *
 #pragma unroll
                         for (int h = 0; h < 2; ++h) {
                             const int r = r0 + s * STEP;
-                            const f32x4 x = own[r * 16 + ((c + h) ^ (r & 15))];
+                            const f32x4 x = own[r * 16 + ((c + (apart ? 8 * h : h)) ^ (r & 15))];
                             f32x4 y = {};
                             if constexpr (GATED) y = own[r * 16 + ((8 + c + h) ^ (r & 15))];
 #pragma unroll
@@ -569,13 +571,13 @@ __global__ __launch_bounds__(64 * WM * WN, WM * WN / 4 * (2 * BUFS * (BM + BN) *
                                     w[1] = pack4<MI_E5M2>(z[4] * f, z[5] * f, z[6] * f, z[7] * f);
                                 }
                                 if (WHOLE || m + s * STEP < g.M)
-                                    put_bytes<STREAM>(to + s * (STEP * ldq), WHOLE ? 8 : g.N - n, w);
+                                    put_bytes<STREAM>(to + s * (STEP * ldq), WHOLE ? 64 : g.N - n, w, apart);
                             }
                         };
                         keep(v, GATED ? 0 : wn / SHARE, g.z, g.ldz);
                         if constexpr (GATED) keep(u, 1, g.zu, g.ldzu);
                     }
-                    put_out<T, GATED, R, 8, WHOLE, STREAM>(g, m, STEP, n, v, u);
+                    put_out<T, GATED, R, 8, WHOLE, STREAM, true>(g, m, STEP, n, v, u);
                 }
                 asm volatile("" ::: "memory");
             }
