@@ -137,7 +137,8 @@ template <class T, int N> __device__ __forceinline__ void bias_at(const void *bi
 
 // N values or bytes to memory, past L2 where they STREAM: a large product's
 // outputs would push out operands that neighbours read (8192 x 8192 x 4096 with
-// an 8-bit checkpoint 400 us, 417 through L2; gated 744 and 761).
+// an 8-bit checkpoint 430 us, 445 through L2; gated with two 834 and 860, but 915
+// where the checkpoints' pieces of 32 bytes pass it too: those L2 has to join).
 template <class CT, int N, bool STREAM> __device__ __forceinline__ void put(CT *p, int left, const float (&v)[N]) {
     if (STREAM && left >= N) {
         typedef typename Values<CT, N>::type type;

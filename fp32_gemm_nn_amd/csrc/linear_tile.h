@@ -571,7 +571,7 @@ __global__ __launch_bounds__(64 * WM * WN, WM * WN / 4 * (2 * BUFS * (BM + BN) *
                                     w[1] = pack4<MI_E5M2>(z[4] * f, z[5] * f, z[6] * f, z[7] * f);
                                 }
                                 if (WHOLE || m + s * STEP < g.M)
-                                    put_bytes<STREAM>(to + s * (STEP * ldq), WHOLE ? 64 : g.N - n, w, apart);
+                                    put_bytes<STREAM && !GATED>(to + s * (STEP * ldq), WHOLE ? 64 : g.N - n, w, apart);
                             }
                         };
                         keep(v, GATED ? 0 : wn / SHARE, g.z, g.ldz);
