@@ -2,6 +2,15 @@
 // f(g) u, and z or g and u as they were kept (in 8 bits with scales, or as
 // matrices), their gradients, f(z) or f(g) u again, and the sums over rows
 // that are the biases' gradients.
+//
+// Bound by memory: 8192 x 8192 gated in BF16 from E4M3, with h, reads 4 and
+// writes 6 bytes a value: 132 us (5.1 TB/s; a large copy reaches 5.4). A
+// workgroup takes 128 columns, which share a scale, of a run of rows; 512 columns
+// at a time took 4% longer, and more rows' reads at once as much more without the
+// gate (66 us for one, 73 for two). The sums cost 4 us there: each workgroup's go
+// through the workspace, and the last of a strip of columns adds them, sixteen
+// reads at once (one by one that took 25 us). 777 x 1300 in FP16 with its sums
+// takes 7.5 us, 64 x 4096 gated with both 5.6: a launch and three memory latencies.
 
 #include <type_traits>
 

@@ -1,5 +1,37 @@
 // Products of many outputs in 16 bits, in tiles of BM x BN whose operands go
 // through LDS. One translation unit for each type includes this.
+//
+// LDS holds BUFS blocks of 64 values of k; whole 16-byte chunks come to it
+// without registers (DIRECT), others through them (STAGED, FAR). A wave forms
+// the products of one half of a block while it reads the operands of the other
+// from LDS, and the waves meet once a block, between the halves: by then all of
+// the block is in registers, so its place takes the block BUFS further, whose
+// loads go between the rows of products. What is on its way to later places
+// stays so at the meeting. Operands in either layout: with k running fastest as
+// they lie, otherwise by LDS's transposing reads, so no layout costs a pass.
+//
+// 256 x 256 outputs on eight waves (64 x 128 each, 128 registers of sums) read
+// the least from L2: 8192 x 8192 x 4096 takes 376 to 414 us by the card (1.33 to
+// 1.46 PFLOP/s; 128 x 256 468, 128 x 128 460 on a card where it took 377), 8192 x
+// 4096 x 8192 with B's outputs running fastest 365 to 410, 4096 x 4096 x 8192
+// with both across 196 to 207. What bounds them is power: the clock falls to 1.7
+// to 1.9 GHz of 2.4, with the matrix cores busy 62 to 68% of the time, and
+// operands of zeros take 296 us instead of 391. So what saves energy counts, not
+// what fills gaps: raised wave priority and other orders of reads and loads
+// changed it by 1%, v_mfma_f32_32x32x16 (413 us for 378) by its reads of sums.
+// Below a round of 256 such tiles the smaller ones win: 128 x 128 outputs on
+// eight waves, two workgroups to a CU (2048 x 4096 x 1024: 19.2 us, 28.9 in 256 x
+// 256) or one with four blocks in LDS (2048 x 2048 x 4096: 36.6 us, 47.6 with
+// two), and 64 x 128 (512 x 2048 x 2048: 12.3 us, 16.4 in 128 x 128). Four waves
+// on 128 x 128 outputs take longer (20.0 us for 19.2; 46 for 37).
+//
+// The gated tile takes as many rows of both weights, each wave of the same
+// columns, so that f(g) u needs no exchange: 8192 x 8192 x 4096 takes 744 to 776
+// us (1.42 to 1.48 PFLOP/s), with both projections kept in 8 bits 834 to 838.
+// What is kept costs its bytes, which all CUs write at once at a tile's end.
+//
+// Rows without whole chunks cost registers and addresses: 4096 x 4096 x 4096 with
+// rows 8 bytes aligned takes 142 us in tiles of 256 x 128, 98 in aligned ones.
 #ifndef MISGEMM_LINEAR_TILE_H
 #define MISGEMM_LINEAR_TILE_H
 

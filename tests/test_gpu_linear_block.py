@@ -244,3 +244,45 @@ def test_sizes_that_end_everywhere(ta, tb):
         torch.cuda.synchronize()
         x, y = (t.double().T.contiguous() if f == "T" else t.double() for t, f in ((a, ta), (b, tb)))
         assert torch.equal(c.double(), x @ y), (M, N, K)
+
+
+@pytest.mark.parametrize("out", [BF, torch.float32])
+@pytest.mark.parametrize("M,N,K", [(4096, 4096, 1024), (1030, 2060, 512), (300, 500, 200), (130, 130, 2048), (40, 500, 200), (1, 500, 200)])
+def test_outputs_at_any_alignment(M, N, K, out):
+    """Aligned operands, and outputs and a residual whose rows lie anywhere: nothing beside them is written."""
+    g = gen(7)
+    a, w, u = (torch.randint(-1, 2, (r, K), generator=g, device="cuda") * (torch.arange(K, device="cuda") % max(1, K // 200) == 0) for r in (M, N, N))
+    a, w, u = (t.to(BF) for t in (a, w, u))          # sums of at most 200: whole numbers that BF16 holds
+
+    def place(dtype):
+        raw = torch.full((M * (N + 1) + 9,), 77.0, dtype=dtype, device="cuda")
+        return raw, raw[1:1 + M * (N + 1)].view(M, N + 1)[:, :N]
+
+    def beside(raw, t):
+        v = raw.clone()
+        v[1:1 + M * (N + 1)].view(M, N + 1)[:, :N] = 77.0
+        return bool((v == 77.0).all())
+    (rc, c), (rz, z), (rr, r) = place(out), place(out), place(out)
+    r.copy_(torch.randint(-9, 10, (M, N), generator=g, device="cuda"))
+    x, y = (a.double() @ t.double().T.contiguous() for t in (w, u))
+    mg.linear("N", "T", 1.0, a, w, 1.0, c, residual=r, z=z, act="relu")
+    torch.cuda.synchronize()
+    assert torch.equal(z.double(), x) and torch.equal(c.double(), (x.clamp(min=0) + r.double()).to(out).double())
+    assert all(beside(*p) for p in ((rc, c), (rz, z), (rr, r)))
+    mg.gated(a, w, u, c, act="relu", g=z, u=r)
+    torch.cuda.synchronize()
+    assert torch.equal(z.double(), x) and torch.equal(r.double(), y) and torch.equal(c.double(), (x.clamp(min=0) * y).to(out).double())
+    assert all(beside(*p) for p in ((rc, c), (rz, z), (rr, r)))
+    q = [torch.full((M * (N + 3) + 9,), 0x5B, dtype=torch.uint8, device="cuda") for _ in range(2)]
+    p, p2 = (t[5:5 + M * (N + 3)].view(M, N + 3)[:, :N].view(torch.float8_e4m3fn) for t in q)
+    s, s2, want, ws = *(torch.empty((N + 127) // 128, M, device="cuda") for _ in range(2)), *mg.fp8_empty(M, N)
+    mg.gated(a, w, u, c, act="none", g=p, scale_g=s, u=p2, scale_u=s2)
+    mg.fp8_quantize(x.float(), want, ws)
+    torch.cuda.synchronize()
+    assert torch.equal(p.view(torch.uint8), want.view(torch.uint8)) and torch.equal(s, ws)
+    mg.fp8_quantize(y.float(), want, ws)
+    torch.cuda.synchronize()
+    assert torch.equal(p2.view(torch.uint8), want.view(torch.uint8)) and torch.equal(s2, ws)
+    for t in q:
+        t[5:5 + M * (N + 3)].view(M, N + 3)[:, :N] = 0x5B
+        assert (t == 0x5B).all()
