@@ -286,3 +286,33 @@ def test_outputs_at_any_alignment(M, N, K, out):
     for t in q:
         t[5:5 + M * (N + 3)].view(M, N + 3)[:, :N] = 0x5B
         assert (t == 0x5B).all()
+
+
+@pytest.mark.parametrize("type", [BF, torch.float16])
+@pytest.mark.parametrize("ta,tb", ["NT", "NN", "TN", "TT"])
+def test_sizes_of_every_tile(ta, tb, type):
+    """From outputs that few workgroups share to those that fill the card, k whole and shared: each tile size in turn.
+    Whole numbers, K not a whole number of blocks; outputs in FP32 (exact) and in the operands' type (rounded once)."""
+    g = gen(8)
+    for M, N, K in ((104, 4208, 544), (112, 4176, 1616), (3440, 4752, 328), (2960, 2600, 328), (4216, 416, 328), (4792, 200, 2544), (4304, 136, 3032),
+                    (4272, 904, 328), (3344, 2328, 328), (1752, 4640, 328)):
+        a, b = (torch.randint(-4, 5, (c, r) if t == "T" else (r, c), generator=g, device="cuda").to(type) for r, c, t in ((M, K, ta), (K, N, tb)))
+        x, y = (t.double().T.contiguous() if f == "T" else t.double() for t, f in ((a, ta), (b, tb)))
+        want = x @ y
+        for out in (torch.float32, type):
+            c = torch.full((M, N), float("nan"), dtype=out, device="cuda")
+            mg.linear(ta, tb, 1.0, a, b, 0.0, c)
+            torch.cuda.synchronize()
+            assert torch.equal(c, want.to(out)), (M, N, K, out)
+
+
+@pytest.mark.parametrize("type", [BF, torch.float16])
+def test_gated_sizes_of_every_tile(type):
+    g = gen(9)
+    for M, N, K in ((400, 4240, 344), (40, 4216, 3152), (72, 4392, 520), (104, 2080, 2280), (2624, 248, 336), (608, 3272, 328), (904, 4264, 328)):
+        a, w, u = (torch.randint(-4, 5, (r, K), generator=g, device="cuda").to(type) for r in (M, N, N))
+        x, y = (a.double() @ t.double().T.contiguous() for t in (w, u))
+        c, z, z2 = (torch.full((M, N), float("nan"), device="cuda") for _ in range(3))
+        mg.gated(a, w, u, c, act="relu", g=z, u=z2)
+        torch.cuda.synchronize()
+        assert torch.equal(z.double(), x) and torch.equal(z2.double(), y) and torch.equal(c, (x.clamp(min=0) * y).float()), (M, N, K)
