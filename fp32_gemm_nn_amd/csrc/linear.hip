@@ -180,7 +180,7 @@ extern "C" int mi_linear(char transA, char transB, int type, int M, int N, int K
     g.M = M;
     g.N = N;
     g.K = reads ? K : 0;
-    g.alpha = alpha;
+    g.alpha = reads ? alpha : 0.0f;   // without a sum an infinite alpha has no part in z either
     g.beta = beta;
     g.act = act;
     g.ztype = ztype;
