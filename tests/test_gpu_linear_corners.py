@@ -1,4 +1,8 @@
-"""Corners of the feed-forward block's operators on the GPU: products of nothing whatever alpha is."""
+"""Corners of the feed-forward block's operators on the GPU: products of nothing whatever alpha is, and 8-bit checkpoints
+from the largest tiles.
+
+Tolerances count roundings of 2^-24 in FP32.
+"""
 import math
 import sys
 
@@ -9,7 +13,7 @@ import fp32_gemm_nn_amd as mg
 torch = pytest.importorskip("torch")
 pytestmark = pytest.mark.gpu
 
-from test_gpu_fp8 import Framed, gen, values  # noqa: E402
+from test_gpu_fp8 import F8, U32, Framed, blocks, gen, values  # noqa: E402
 
 BF, F32 = torch.bfloat16, torch.float32
 
@@ -46,3 +50,38 @@ def test_no_k_whatever_alpha(M, N, alpha):
         mg.fp8_quantize(want.contiguous(), q2, s2)
         torch.cuda.synchronize()
         assert torch.equal(c.t, want) and torch.equal(q.view(torch.uint8), q2.view(torch.uint8)) and torch.equal(s, s2)
+
+
+@pytest.mark.parametrize("kind", ["e4m3", "e5m2"])
+@pytest.mark.parametrize("out", [BF, F32])
+@pytest.mark.parametrize("ta,tb", ["NT", "NN", "TN", "TT"])
+def test_kept_in_8_bits_from_the_largest_tiles(ta, tb, out, kind):
+    """Enough outputs for tiles of 256 x 256 (of whole 16 bytes) or 256 x 128 (others), inside the matrix and over both of its
+    edges, blocks of k that end early; rows and blocks of columns whose scales differ. The checkpoint is bit for bit what quantising
+    z in FP32 gives, z as the same call keeps it in 32 bits, at any alignment."""
+    for M, N, K, pad in ((2552, 4088, 136, 0), (4088, 3048, 136, 0), (2040, 3001, 520, 1)):
+        g = gen(M)
+        rows = torch.exp2(torch.randint(-8, 9, (M, 1), generator=g, device="cuda").float())
+        a = torch.randint(-3, 4, (M, K), generator=g, device="cuda") * rows
+        b = torch.randint(-3, 4, (N, K), generator=g, device="cuda").float()
+        b[128:256] *= 2.0**20                   # a block of columns whose scale is another
+        a, b = (Framed(*t.shape, BF, t.shape[1] + pad, pad).fill(t).t for t in (a.T if ta == "T" else a, b if tb == "T" else b.T))
+        bias = torch.randint(-9, 10, (N,), generator=g, device="cuda") / 2
+        x, y = (t.double().T.contiguous() if f == "T" else t.double() for t, f in ((a, ta), (b, tb)))
+        z = Framed(M, N, F32, N + 1, 1)
+        mg.linear(ta, tb, 1.0, a, b, 0.0, torch.empty(M, N, device="cuda"), bias=bias, act="relu", z=z.t)
+        # At most K + 64 additions, each off by a whole step inside the matrix cores.
+        assert ((z.t.double() - x @ y - bias.double()).abs() <= (x.abs() @ y.abs() + bias.double().abs()) * ((K + 64) * 2 * U32)).all()
+        q, s = Framed(M, N, F8[kind], N + 5, 3), Framed(blocks(N), M, F32, M + 3, 1)
+        c, r = Framed(M, N, out, N + 3, 1), values(g, M, N, out)
+        mg.linear(ta, tb, 1.0, a, b, 1.0, c.t, bias=bias, act="relu", residual=r, z=q.t, scale=s.t)
+        q2, s2 = Framed(M, N, F8[kind]), Framed(blocks(N), M, F32)
+        mg.fp8_quantize(z.t, q2.t, s2.t)
+        torch.cuda.synchronize()
+        assert torch.equal(s.t, s2.t), (M, N, K)
+        off = q.t.view(torch.uint8) != q2.t.view(torch.uint8)
+        assert not off.any(), (M, N, K, int(off.sum()), off.nonzero()[:4].tolist())
+        # The residual is added in FP32 (one rounding), and the sum rounded to its type.
+        want = z.t.clamp(min=0) + r.float()
+        assert torch.equal(c.t, want.to(out)), (M, N, K)
+        assert q.whole() and s.whole() and c.whole() and z.whole()
