@@ -1,5 +1,5 @@
-"""Corners of the feed-forward block's operators on the GPU: products of nothing whatever alpha is, and 8-bit checkpoints
-from the largest tiles.
+"""Corners of the feed-forward block's operators on the GPU: products of nothing whatever alpha is, 8-bit checkpoints from
+the largest tiles, and activations' derivatives where they are small.
 
 Tolerances count roundings of 2^-24 in FP32.
 """
@@ -85,3 +85,47 @@ def test_kept_in_8_bits_from_the_largest_tiles(ta, tb, out, kind):
         want = z.t.clamp(min=0) + r.float()
         assert torch.equal(c.t, want.to(out)), (M, N, K)
         assert q.whole() and s.whole() and c.whole() and z.whole()
+
+
+def slope64(z, act):
+    """f'(z), and how far FP32 may be off. u = 2^-24 is a rounding; v_exp_f32 and v_rcp_f32 are off by 2 u of their result.
+
+    With s = 1 / (1 + e^-p), of which the exponent takes `arg` |p| u (its roundings) and the rest 5: s is off by
+    s ((1 - s) (arg |p| + 2) + 3) u, and exact (1) where e^-p < 2^-25, so that 1 + e^-p is 1.
+    """
+    z, u = z.double(), U32
+    if act == "gelu":
+        # Phi(-|z|): the polynomial (21 u by its coefficients' sum, 1 u of approximation), its argument (3 u times at most
+        # 2.4), e^(-z^2/2) (1.5 z^2 + 2) u, two products. The other part: a product and a constant, and that e again.
+        h = torch.erfc(z.abs() / math.sqrt(2)) / 2
+        b = z * torch.exp(-z * z / 2) / math.sqrt(2 * math.pi)
+        df = torch.where(z > 0, 1 - h, h) + b
+        return df, h * (34 + 1.5 * z * z) * u + (z > 0) * u + b.abs() * (6 + 1.5 * z * z) * u + df.abs() * u
+    k1, k3 = math.sqrt(8 / math.pi), 0.044715 * math.sqrt(8 / math.pi)
+    p, dp, arg = (z, torch.ones_like(z), 2) if act == "silu" else (k1 * z + k3 * z**3, k1 + 3 * k3 * z * z, 6)
+    e = torch.exp(-p.clamp(-700, 700))
+    s, w = 1 / (1 + e), e / (1 + e)             # w = 1 - s
+    one = p > 25 * math.log(2) + 0.1
+    n = w * (arg * p.abs() + 2) + 3
+    es, ew = torch.where(one, w, s * n * u), torch.where(one, w, (s * n + w) * u)
+    b = z * dp * s * w
+    df = s + b
+    if act == "silu":       # s (1 + z w)
+        return df, s * (z.abs() * ew + (1 + z * w).abs() * u) + (1 + z * w).abs() * es + df.abs() * u
+    # dp is off by 4 u; three products.
+    return df, es + (z * dp).abs() * (s * ew + es * w) + b.abs() * 7 * u + df.abs() * u
+
+
+@pytest.mark.parametrize("act", ["silu", "gelu", "gelu_tanh"])
+def test_slopes_where_they_are_small(act):
+    """f' relative to its parts, down to 2^-118, where v_exp_f32 and v_rcp_f32 may have given 0 for one below 2^-126."""
+    z = torch.cat([torch.linspace(-110, 20, 130001), torch.linspace(-14, 8, 220001), torch.linspace(-1.5, -0.5, 20001),
+                   10.0 ** torch.linspace(-38, 2, 1001), -(10.0 ** torch.linspace(-38, 2, 1001))]).cuda()[None]
+    one, dz, dg, du, h = torch.ones_like(z), *(torch.empty_like(z) for _ in range(4))
+    mg.act_backward(one, z, dz, act=act)
+    mg.gated_backward(one, z, one, dg, du, act=act, h=h)
+    torch.cuda.synchronize()
+    want, limit = slope64(z, act)
+    over = (dz.double() - want).abs() / (limit + 2.0**-118)
+    assert over.max() <= 1, (float(over.max()), float(z.flatten()[over.argmax()]))
+    assert torch.equal(dg, dz) and torch.equal(du, h)
