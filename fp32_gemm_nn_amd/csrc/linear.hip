@@ -98,9 +98,10 @@ int pick(LinArgs &g, bool gated, bool ta, bool tb) {
         if (c->kernel < 16 ? !few || tiles * 64 * c->waves >= 1LL << 32 : c->kernel >= 24 ? !g.direct : c->kernel > 16 && !g.near) continue;
         if (gated && g.zs != nullptr && c->bn < kBlock) continue;   // a scale's columns are in one workgroup
         const Fit &f = c->fit[c->kernel < 16 ? !g.direct : !kmajor];
-        // At least three blocks of k for each workgroup, and three workgroups to a CU at most.
+        // At least three blocks of k for each workgroup, three workgroups to a CU at most, and parts that fit the workspace.
         auto shared = [&](int splits) {
-            return c->split > 0.0f && splits <= 16 && kblocks / splits >= 3 && tiles * splits <= 3 * kNumCus;
+            return c->split > 0.0f && splits <= 16 && kblocks / splits >= 3 && tiles * splits <= 3 * kNumCus &&
+                   parts_fit(tiles, splits, c->bm * c->bn * (gated ? 2 : 1));
         };
         for (int splits = 1; splits == 1 || shared(splits); splits *= 2) {
             const float groups = (float)(tiles * splits);

@@ -627,10 +627,8 @@ int launch_tile(LinArgs &g, hipStream_t stream) {
     g.tiles_n = (g.N + COLS - 1) / COLS;
     const int kblocks = (g.K + kStep - 1) / kStep;
     const long long tiles = (long long)g.tiles_m * g.tiles_n;
-    // What was chosen, where a tile's parts fit the workspace and there is one.
-    if (g.splits > 1 && (tiles * g.splits * BM * BN > (long long)misgemm_workspace::kFloats ||
-                         tiles > misgemm_workspace::kCounters || !misgemm_workspace::get(stream, &g.ws, &g.counters)))
-        g.splits = 1;
+    // What was chosen (its parts fit), where the stream has a workspace.
+    if (g.splits > 1 && !misgemm_workspace::get(stream, &g.ws, &g.counters)) g.splits = 1;
     g.kb_per_split = (kblocks + g.splits - 1) / g.splits;
     if (g.splits > 1) g.splits = (kblocks + g.kb_per_split - 1) / g.kb_per_split;
     hipLaunchKernelGGL((lin_tile<T, BM, BN, WM, WN, BUFS, KA, KB, GATED, WAY>), dim3((unsigned)(tiles * g.splits)),
