@@ -129,3 +129,26 @@ def test_slopes_where_they_are_small(act):
     over = (dz.double() - want).abs() / (limit + 2.0**-118)
     assert over.max() <= 1, (float(over.max()), float(z.flatten()[over.argmax()]))
     assert torch.equal(dg, dz) and torch.equal(du, h)
+
+
+@pytest.mark.parametrize("type", [BF, F32])
+@pytest.mark.parametrize("rows,cols", [(100003, 64), (70000, 136), (40001, 384), (70001, 9)])
+def test_backward_of_narrow_matrices(rows, cols, type):
+    """Many rows of few columns, cut into more parts than others: whole numbers, exact whatever the order."""
+    g = gen(rows)
+    dy, z, u = (torch.randint(-2, 3, (rows, cols), generator=g, device="cuda").to(type) for _ in range(3))
+    out = [Framed(rows, cols, type, cols + 3, 1) for _ in range(3)]
+    sums = torch.full((3, cols), 2.0, device="cuda")
+    d64, u64, f64 = dy.double(), u.double(), z.double().clamp(min=0)
+    on = (z > 0).double()
+    for b in (None, sums[0]):
+        mg.act_backward(dy, z, out[0].t, act="relu", y=out[1].t, dbias=b, beta=0.5)
+        torch.cuda.synchronize()
+        assert torch.equal(out[0].t.double(), d64 * on) and torch.equal(out[1].t.double(), f64)
+    for b, b2 in ((None, None), (sums[1], sums[2])):
+        mg.gated_backward(dy, z, u, out[0].t, out[1].t, act="relu", h=out[2].t, dbias_g=b, dbias_u=b2, beta=0.5)
+        torch.cuda.synchronize()
+        assert all(torch.equal(o.t.double(), w) for o, w in zip(out, (d64 * u64 * on, d64 * f64, f64 * u64)))
+    for got, want in zip(sums, (d64 * on, d64 * u64 * on, d64 * f64)):
+        assert torch.equal(got.double(), want.sum(0) + 1)
+    assert all(o.whole() for o in out)

@@ -77,3 +77,20 @@ def test_without_a_workspace_nothing_is_shared(tmp_path, state):
     calls = [(name, [*a, on]) for name, a in calls]
     got = plans(calls, tmp_path, **state)
     assert all(p is None or p[4] == 1 for p in got) and sum(p is not None for p in got) >= 6
+
+
+@pytest.mark.parametrize("rows,cols", [(1000000, 64), (1000000, 128), (300000, 500), (200000, 136), (8192, 8192), (4096, 40), (70, 70), (1, 1)])
+def test_backward_of_narrow_matrices_fills_the_card(tmp_path, rows, cols):
+    """However few columns, rows are cut into parts for each CU: of 64 rows at least, of 512 where biases' gradients join them, which
+    are no more than have room."""
+    calls = [("mi_act_backward", [1, rows, cols, P, cols, 2, 1, P, cols, 0, 0, P, cols, 0, 0, 0.0, 0], {}),
+             ("mi_gated_backward", [1, rows, cols, P, cols, 2, 1, P, cols, 0, 0, P, cols, 0, 0, P, cols, P, cols, 0, 0, 0.0, 0, 0], {}),
+             ("mi_act_backward", [1, rows, cols, P, cols, 2, 1, P, cols, 0, 0, P, cols, 0, 0, 0.0, P], {}),
+             ("mi_gated_backward", [1, rows, cols, P, cols, 2, 1, P, cols, 0, 0, P, cols, 0, 0, P, cols, P, cols, 0, 0, 0.0, P, P], {})]
+    got = launches(calls, tmp_path)
+    assert all(rc == 0 for rc, _ in got)
+    for least, (_, each) in zip((64, 64, 512, 512), got):
+        x, y, _ = each[-1].grid
+        assert x == -(-cols // 128) and 1 <= y <= max(64, -(-rows // least))
+        assert x * y >= min(256, x * (rows // least))
+    assert all(2 * each[-1].grid[1] * cols <= FLOATS for _, each in got[2:])
