@@ -28,7 +28,7 @@ extern "C" {
 
 /* Activations f, and their derivatives f'. In FP32. f(-inf) and f(inf) are
  * their limits: 0 and inf (MI_ACT_NONE: -inf and inf); so are f'. NaN stays.
- * What lies below 2^-119 may come as 0. */
+ * f below 2^-119 and f' below 2^-118 may come as 0. */
 #define MI_ACT_NONE       0   /* z */
 #define MI_ACT_RELU       1   /* max(z, 0); f'(0) = 0 */
 #define MI_ACT_SILU       2   /* z / (1 + e^-z) */
