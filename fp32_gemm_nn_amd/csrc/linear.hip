@@ -39,9 +39,13 @@ bool whole(const void *p, long long ld, bool kmajor, int across) {
 // (one for each CU), a step a block of 64 values of k for each of a workgroup's
 // waves that split it. The constants are fitted to the measured times of all
 // kernels on 1000 shapes (M, N and K from 1, 64 and 64 to 8192, all layouts and
-// alignments), which they reproduce to 5-19%; the kernel picked was 1.6% slower
-// than the fastest on average, 9% in one case of twenty, 36% at worst (the gated
-// 3460 x 80 x 944: 17.4 us with k split by four, 12.8 in another tile).
+// alignments), each with one set of operands again and again, which the caches
+// hold where it fits. They reproduce these to 5-19%; the kernel picked was 1.6%
+// slower than the fastest on average, 9% in one case of twenty, 36% at worst (the
+// gated 3460 x 80 x 944: 17.4 us with k split by four, 12.8 in another tile). On
+// 200 other shapes, measured alike, 11% in one case of twenty and 22% at worst. On
+// 70 of up to 96 rows with operands in rotation, which come from memory, 2.2% on
+// average, 10% in one of twenty, 18% at worst.
 struct Fit {
     float first, round, step, share;
 };

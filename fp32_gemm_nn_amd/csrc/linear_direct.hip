@@ -7,10 +7,10 @@
 // sums are added in order of wave. A wave has D blocks of k on their way in
 // registers. It reads them as whole rows of 128 bytes, eight to a load, and
 // turns them into the matrix cores' operands (lane i of 16 holds row i) through
-// LDS of its own, which needs no barrier. 1 x 4096 x 8192 takes 11.4 us (5.9
-// TB/s) where 64 x 128 tiles take 24.5, 33 x 4096 x 4096 8.1 us and 21.8, the
-// gated 1 x 8192 x 4096 20.3 us (6.6 TB/s) and 33.4; with weights that the last
-// level of cache does not hold, 27.5 us (4.9 TB/s).
+// LDS of its own, which needs no barrier. 1 x 4096 x 8192 takes 11.6 us (5.8
+// TB/s) where 64 x 128 tiles take 17.2 with k in eight parts, 33 x 4096 x 4096 9.2
+// us and 13.8, the gated 1 x 8192 x 4096 21.2 us (6.3 TB/s) and 26.8; with weights
+// that the last level of cache does not hold, 13.4, 12.0 and 26.6 us.
 
 #include <type_traits>
 

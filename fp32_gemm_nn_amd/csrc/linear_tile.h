@@ -19,19 +19,20 @@
 // operands of zeros take 296 us instead of 391. So what saves energy counts, not
 // what fills gaps: raised wave priority and other orders of reads and loads
 // changed it by 1%, v_mfma_f32_32x32x16 (413 us for 378) by its reads of sums.
-// Below a round of 256 such tiles the smaller ones win: 128 x 128 outputs on
-// eight waves, two workgroups to a CU (2048 x 4096 x 1024: 19.2 us, 28.9 in 256 x
-// 256) or one with four blocks in LDS (2048 x 2048 x 4096: 36.6 us, 47.6 with
-// two), and 64 x 128 (512 x 2048 x 2048: 12.3 us, 16.4 in 128 x 128). Four waves
-// on 128 x 128 outputs take longer (20.0 us for 19.2; 46 for 37).
+// Below a round of 256 such tiles the smaller ones win: 128 x 256 outputs or 128
+// x 128 on eight waves, of these two workgroups to a CU (2048 x 4096 x 1024: 19.8
+// us in both, 24.3 in 256 x 256) or one with four blocks in LDS (2048 x 2048 x
+// 4096: 34.5 to 37.5 us, 43 with two), and 64 x 128 (512 x 2048 x 2048: 12.1 us, k
+// shared by two, 15 in 128 x 128). Four waves on 128 x 128 outputs take longer
+// (20.0 us for 19.2; 46 for 37).
 //
 // The gated tile takes as many rows of both weights, each wave of the same
 // columns, so that f(g) u needs no exchange: 8192 x 8192 x 4096 takes 744 to 776
-// us (1.42 to 1.48 PFLOP/s), with both projections kept in 8 bits 834 to 838.
+// us (1.42 to 1.48 PFLOP/s), with both projections kept in 8 bits 823 to 840.
 // What is kept costs its bytes, which all CUs write at once at a tile's end.
 //
 // Rows without whole chunks cost registers and addresses: 4096 x 4096 x 4096 with
-// rows 8 bytes aligned takes 142 us in tiles of 256 x 128, 98 in aligned ones.
+// rows 8 bytes aligned takes 142 to 150 us in tiles of 256 x 128, 98 in aligned ones.
 #ifndef MISGEMM_LINEAR_TILE_H
 #define MISGEMM_LINEAR_TILE_H
 
