@@ -10,7 +10,7 @@
 // gate (66 us for one, 73 for two). The sums cost 4 us there: each workgroup's go
 // through the workspace, and the last of a strip of columns adds them, sixteen
 // reads at once (one by one that took 25 us). 777 x 1300 in FP16 with its sums
-// takes 7.5 us, 64 x 4096 gated with both 5.6: a launch and three memory latencies.
+// takes 7.9 us, 64 x 4096 gated with both 5.7: a launch and three memory latencies.
 
 #include <type_traits>
 

@@ -75,12 +75,13 @@ json.dump(out, sys.stdout)
 
 
 class Launch:
-    """A kernel by its name and the numbers of its template, its grid, and its threads."""
+    """A kernel by its name and the numbers of its template (truth values and enumerators too), its grid, and its threads."""
 
     def __init__(self, name, x, y, z, threads):
         self.name, self.grid, self.threads = name, (x, y, z), threads
-        self.kernel = re.search(r"\d([a-z][a-z0-9_]*)I", name).group(1) if re.search(r"\d([a-z][a-z0-9_]*)I", name) else name
-        self.numbers = [int(v) for v in re.findall(r"L(?:i|b|NS[0-9_]*\d*\w*?E)(\d+)E", name)]
+        template = re.search(r"\d([a-z][a-z0-9_]*)I", name)
+        self.kernel = template.group(1) if template else name
+        self.numbers = [int(v) for v in re.findall(r"L(?:i|b|N\w*?E)(\d+)E", name)]
 
     def __repr__(self):
         return f"{self.kernel}{self.numbers} {self.grid}"
